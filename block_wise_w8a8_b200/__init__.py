@@ -15,7 +15,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw8a8.so")
 
-PATH_INT8, PATH_BF16, PATH_NONE = 0, 1, 2
+PATH_INT8, PATH_BF16, PATH_NONE, PATH_FP4 = 0, 1, 2, 3
 DEVERR_NONE, DEVERR_TIMEOUT = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "shape", 3: "not device memory",
            4: "alignment", 5: "workspace", 6: "CUDA error"}
@@ -30,6 +30,12 @@ class W8A8Error(RuntimeError):
 class _Weight(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("w_bf16", ctypes.c_void_p),
                 ("wq", ctypes.c_void_p), ("ws", ctypes.c_void_p)]
+
+
+class _FP4Weight(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("w_bf16", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("factor", ctypes.c_void_p)]
 
 
 _lib = None
@@ -72,6 +78,25 @@ _SIGS = {
     "w8a8_rowwise_linear": [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                             ctypes.c_void_p, ctypes.c_void_p],
+    "w8a8_fp4_quantize": [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+    "w8a8_fp4_dequantize": [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                            ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p],
+    "w8a8_fp4_linear": [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(_FP4Weight),
+                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                        ctypes.POINTER(ctypes.c_int), ctypes.c_void_p],
+    "w8a8_fp4_linear_prequant": [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                 ctypes.c_int64, ctypes.POINTER(_FP4Weight), ctypes.c_void_p,
+                                 ctypes.c_void_p, ctypes.c_void_p],
+    "w8a8_block_norm": [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                        ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int64,
+                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+    "w8a8_block_norm_fp4": [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int64,
+                            ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
 }
 
 
@@ -93,6 +118,10 @@ def lib():
         L.w8a8_linear_host_workspace_bytes.restype = ctypes.c_size_t
         L.w8a8_linear_host_chunk_rows.argtypes = [ctypes.c_int64] * 2
         L.w8a8_linear_host_chunk_rows.restype = ctypes.c_int64
+        L.w8a8_fp4_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+        L.w8a8_fp4_scale_bytes.restype = ctypes.c_size_t
+        L.w8a8_fp4_linear_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+        L.w8a8_fp4_linear_workspace_bytes.restype = ctypes.c_size_t
         L.w8a8_device_error.argtypes = []
         L.w8a8_device_error.restype = ctypes.c_int
         L.w8a8_last_cuda_error.argtypes = []
@@ -448,6 +477,257 @@ def bf16_linear(x, w, bias=None, out=None):
     _check("w8a8_bf16_linear", lib().w8a8_bf16_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(out),
                                                        M, K, N, _stream(x.device)))
     return out
+
+
+# ---- the microscaled 4-bit linear and the norms around a block -----------------------------
+FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+_FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+
+
+def _fp4_format(format):
+    if format not in FP4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP4_FORMATS)}, got {format!r}")
+    return FP4_FORMATS[format]
+
+
+def _fp4_k(K):
+    if K <= 0 or K % 32:
+        raise ValueError(f"K must be a positive multiple of 32, got {K}")
+
+
+def _fp4_tiles(rows, K, format):
+    """Shape of a quantized matrix's scales: tiles of 128 rows x 4 blocks, 512 bytes each."""
+    return (-(-rows // 128), -(-K // (4 * _FP4_BLOCK[format])), 512)
+
+
+class FP4Tensor:
+    """A matrix [rows, K] in 4-bit floating point: codes uint8 [rows, K/2] (two a byte, the
+    even element in the low half), scales uint8 in the tiled layout of include/w8a8.h, and
+    for "nvfp4" the rows' float32 factors (None for "mxfp4")."""
+
+    __slots__ = ("codes", "scales", "factor", "format", "rows", "K", "device")
+
+    def __init__(self, codes, scales, factor, format):
+        fmt = _fp4_format(format)
+        _need(codes, torch.uint8, "codes")
+        rows, half = codes.shape
+        _fp4_k(2 * half)
+        self.rows, self.K, self.format, self.device = rows, 2 * half, format, codes.device
+        _in(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device, "scales")
+        if fmt:
+            _in(factor, (rows,), torch.float32, codes.device, "factor")
+        elif factor is not None:
+            raise ValueError("mxfp4 has no row factors")
+        self.codes, self.scales, self.factor = codes, scales, factor
+
+
+def _fp4_empty(rows, K, format, device):
+    """A quantized matrix of this size, to be written."""
+    _fp4_k(K)
+    q = FP4Tensor.__new__(FP4Tensor)
+    q.rows, q.K, q.format, q.device = rows, K, format, device
+    q.codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
+    q.scales = torch.empty(_fp4_tiles(rows, K, format), dtype=torch.uint8, device=device)
+    q.factor = torch.empty((rows,), dtype=torch.float32, device=device) if format == "nvfp4" else None
+    return q
+
+
+def _fp4_out(out, rows, K, format, device):
+    if out is None:
+        return _fp4_empty(rows, K, format, device)
+    if not isinstance(out, FP4Tensor):
+        raise TypeError("out must be an FP4Tensor")
+    if (out.rows, out.K, out.format) != (rows, K, format) or out.device != device:
+        raise ValueError(f"out must be [{rows}, {K}] {format} on {device}")
+    return out
+
+
+def fp4_tile_scales(scales):
+    """Block scales [rows, blocks] (bytes) -> the tiled layout of FP4Tensor.scales, zeros
+    past the end.  For weights quantized elsewhere; plain tensor operations, once at load."""
+    if scales.dim() != 2 or scales.element_size() != 1:
+        raise ValueError("scales must be a matrix of bytes")
+    R, C = scales.shape
+    rt, ct = -(-R // 128), -(-C // 4)
+    full = torch.zeros((rt * 128, ct * 4), dtype=torch.uint8, device=scales.device)
+    full[:R, :C] = scales.contiguous().view(torch.uint8)
+    return full.view(rt, 4, 32, ct, 4).permute(0, 3, 2, 1, 4).reshape(rt, ct, 512).contiguous()
+
+
+def fp4_untile_scales(tiles, rows, blocks):
+    """The inverse of fp4_tile_scales: bytes [rows, blocks]."""
+    rt, ct, _ = tiles.shape
+    return tiles.view(rt, ct, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(rt * 128, ct * 4)[:rows, :blocks]
+
+
+def fp4_quantize(x, format="nvfp4", out=None):
+    """BF16 [rows, K] -> FP4Tensor, K a multiple of 32.  "mxfp4": blocks of 32 along K with a
+    power-of-two scale; "nvfp4": blocks of 16 with an E4M3 scale and a float32 factor per
+    row.  A row's codes depend on that row alone."""
+    fmt = _fp4_format(format)
+    _need(x, torch.bfloat16, "x")
+    rows, K = x.shape
+    q = _fp4_out(out, rows, K, format, x.device)
+    _check("w8a8_fp4_quantize", lib().w8a8_fp4_quantize(
+        x.data_ptr(), rows, K, fmt, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor),
+        _stream(x.device)))
+    return q
+
+
+def fp4_dequantize(q, out=None):
+    """The values an FP4Tensor's codes stand for, BF16 [rows, K]."""
+    if not isinstance(q, FP4Tensor):
+        raise TypeError("q must be an FP4Tensor")
+    y = _out(out, (q.rows, q.K), torch.bfloat16, q.device, "out")
+    _check("w8a8_fp4_dequantize", lib().w8a8_fp4_dequantize(
+        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), q.rows, q.K, FP4_FORMATS[q.format],
+        y.data_ptr(), _stream(q.device)))
+    return y
+
+
+class FP4Weight:
+    """A linear layer's weight in 4 bits: quantized from w_bf16 at construction, or given as
+    an FP4Tensor q.  w_bf16 is kept for the guard's BF16 path (K not a multiple of 32);
+    without it those shapes raise.  keep_bf16=False drops it after quantizing."""
+
+    def __init__(self, w_bf16=None, format="nvfp4", q=None, keep_bf16=True):
+        if q is not None:
+            if not isinstance(q, FP4Tensor):
+                raise TypeError("q must be an FP4Tensor")
+            self.N, self.K, self.device, format = q.rows, q.K, q.device, q.format
+            if w_bf16 is not None:
+                _in(w_bf16, (q.rows, q.K), torch.bfloat16, q.device, "w")
+        else:
+            _fp4_format(format)
+            _need(w_bf16, torch.bfloat16, "w")
+            (self.N, self.K), self.device = w_bf16.shape, w_bf16.device
+            if self.K and self.K % 32 == 0:
+                q = fp4_quantize(w_bf16, format)
+                if not keep_bf16:
+                    w_bf16 = None
+        self.w, self.q, self.format = w_bf16, q, format
+        self._rec = _FP4Weight(self.N, self.K, FP4_FORMATS[format],
+                               0 if w_bf16 is None else w_bf16.data_ptr(),
+                               0 if q is None else q.codes.data_ptr(),
+                               0 if q is None else q.scales.data_ptr(),
+                               0 if q is None or q.factor is None else q.factor.data_ptr())
+
+    def record(self):
+        return ctypes.byref(self._rec)
+
+
+def _fp4_weight_on(weight, K, device):
+    if not isinstance(weight, FP4Weight):
+        raise TypeError("weight must be an FP4Weight")
+    if weight.K != K:
+        raise ValueError(f"weight has K = {weight.K}, the activations K = {K}")
+    if weight.device != device:
+        raise ValueError(f"weight is on {weight.device}, the activations on {device}")
+
+
+def fp4_linear_workspace_bytes(M, K, format="nvfp4"):
+    return int(lib().w8a8_fp4_linear_workspace_bytes(M, K, _fp4_format(format)))
+
+
+def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False):
+    """y = x W^T + bias in BF16 with x quantized to the weight's 4-bit format in the call.
+    x: [..., K] BF16 (leading dimensions flattened), any number of rows and outputs.  K not a
+    multiple of 32 takes the BF16 GEMM on the weight's BF16 copy."""
+    _need(x, torch.bfloat16, "x")
+    K = x.shape[-1]
+    M = math.prod(x.shape[:-1])
+    dev = x.device
+    _fp4_weight_on(weight, K, dev)
+    if bias is not None:
+        _in(bias, (weight.N,), torch.bfloat16, dev, "bias")
+    out = _out(out, (*x.shape[:-1], weight.N), torch.bfloat16, dev, "out")
+    if workspace is None:
+        need = fp4_linear_workspace_bytes(M, K, weight.format)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _out(workspace, (workspace.numel(),), torch.uint8, dev, "workspace")
+    path = ctypes.c_int(-1)
+    _check("w8a8_fp4_linear", lib().w8a8_fp4_linear(
+        x.data_ptr(), M, K, weight.record(), _ptr(bias), out.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), ctypes.byref(path), _stream(dev)))
+    return (out, path.value) if return_path else out
+
+
+def fp4_linear_prequant(q, weight, bias=None, out=None):
+    """The 4-bit GEMM on an FP4Tensor (e.g. from block_norm_fp4) of the weight's format."""
+    if not isinstance(q, FP4Tensor):
+        raise TypeError("q must be an FP4Tensor")
+    _fp4_weight_on(weight, q.K, q.device)
+    if weight.format != q.format:
+        raise ValueError(f"weight is {weight.format}, the activations {q.format}")
+    if bias is not None:
+        _in(bias, (weight.N,), torch.bfloat16, q.device, "bias")
+    out = _out(out, (q.rows, weight.N), torch.bfloat16, q.device, "out")
+    _check("w8a8_fp4_linear_prequant", lib().w8a8_fp4_linear_prequant(
+        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), q.rows, q.K, weight.record(),
+        _ptr(bias), out.data_ptr(), _stream(q.device)))
+    return out
+
+
+def _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, h_out):
+    """Checks shared by both forms -> (M, K, T, device, h_out)."""
+    _need(h, torch.bfloat16, "h")
+    M, K = h.shape
+    dev = h.device
+    _in(y, (M, K), torch.bfloat16, dev, "y")
+    if post_gamma is not None and not post_norm:
+        raise ValueError("post_gamma needs post_norm")
+    if post_gamma is not None:
+        _in(post_gamma, (K,), torch.bfloat16, dev, "post_gamma")
+    if pre_gamma is not None:
+        _in(pre_gamma, (K,), torch.bfloat16, dev, "pre_gamma")
+    B = 1
+    for t in (gate, scale, shift):
+        if t is not None:
+            B = t.shape[0]
+            break
+    if B == 0 or M % B:
+        raise ValueError(f"gate, scale and shift must be [B, {K}] with B dividing M = {M}")
+    if gate is not None:
+        _in(gate, (B, K), torch.bfloat16, dev, "gate")
+    if scale is not None:
+        _in(scale, (B, K), torch.bfloat16, dev, "scale")
+    if shift is not None:
+        _in(shift, (B, K), torch.bfloat16, dev, "shift")
+    return M, K, max(M // B, 1), dev, _out(h_out, (M, K), torch.bfloat16, dev, "h_out")
+
+
+def block_norm(h, y, post_gamma=None, gate=None, pre_gamma=None, scale=None, shift=None, *,
+               res_scale=1.0, post_norm=True, eps=1e-6, h_out=None, n_out=None):
+    """The residual update between two blocks and the next block's norm, in one pass:
+    h' = bf16(res_scale * h + gate[b] * u) with u = RMSNorm(y) * post_gamma (u = y without
+    post_norm), n = bf16(RMSNorm(h') * pre_gamma * (1 + scale[b]) + shift[b]).  h, y [M, K],
+    K a multiple of 8; gammas [K]; gate, scale, shift [B, K] with b = m // (M // B); each may
+    be None.  h_out may be h (in place) -> (h', n)."""
+    M, K, T, dev, h_out = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm,
+                                           h_out)
+    n = _out(n_out, (M, K), torch.bfloat16, dev, "n_out")
+    _check("w8a8_block_norm", lib().w8a8_block_norm(
+        h.data_ptr(), y.data_ptr(), int(post_norm), _ptr(post_gamma), _ptr(gate), float(res_scale),
+        _ptr(pre_gamma), _ptr(scale), _ptr(shift), T, float(eps), M, K, h_out.data_ptr(),
+        n.data_ptr(), _stream(dev)))
+    return h_out, n
+
+
+def block_norm_fp4(h, y, format="nvfp4", post_gamma=None, gate=None, pre_gamma=None, scale=None,
+                   shift=None, *, res_scale=1.0, post_norm=True, eps=1e-6, h_out=None, out=None):
+    """block_norm with n quantized as fp4_quantize does, without being stored (the same bits
+    as the two calls); K a multiple of 32 -> (h', FP4Tensor)."""
+    fmt = _fp4_format(format)
+    M, K, T, dev, h_out = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm,
+                                           h_out)
+    q = _fp4_out(out, M, K, format, dev)
+    _check("w8a8_block_norm_fp4", lib().w8a8_block_norm_fp4(
+        h.data_ptr(), y.data_ptr(), int(post_norm), _ptr(post_gamma), _ptr(gate), float(res_scale),
+        _ptr(pre_gamma), _ptr(scale), _ptr(shift), T, float(eps), M, K, fmt, h_out.data_ptr(),
+        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), _stream(dev)))
+    return h_out, q
 
 
 def debug_block_sums(xq, wq, m0=0, rows=None, n0=0, cols=None):

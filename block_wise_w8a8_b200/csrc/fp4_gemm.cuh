@@ -1,0 +1,563 @@
+// fp4_gemm.cuh -- products of two microscaled 4-bit matrices on the block-scaled tensor
+// cores (tcgen05.mma kind::mxf4 / kind::mxf4nvf4):
+//
+//   y[m, n] = bf16( xf[m] wf[n] sum_b sx[m, b] sw[n, b] sum_{k in block b} cx[m, k] cw[n, k] + bias[n] )
+//
+// with FP32 accumulation over all of K in tensor memory; the tensor core applies both block
+// scales, the epilogue the row factors (formats in fp4.cuh; kMx has no row factors) and
+// the bias, and rounds once to BF16.
+//
+// Operands are read as the quantizer writes them: codes [rows, K / 2] by TMA with 128-byte
+// swizzle, 256 elements of K (128 bytes a row) a pipeline stage; scales as whole 512-byte
+// tiles, copied on from shared to tensor memory (tcgen05.cp) in front of the products that
+// use them.  Past the end of K the TMA fills codes with zeros, and the scales of the last
+// partial tile are zeros in memory.
+#pragma once
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "gemm.cuh"
+#include "norm.cuh"
+
+namespace w8a8 {
+namespace fp4 {
+
+constexpr int kSliceK = 256;                             // elements of K a stage
+__host__ __device__ constexpr int scale_tiles_a_slice(int fmt) { return fmt == kMx ? 2 : 4; }
+__host__ __device__ constexpr int scale_slice_bytes(int fmt) { return scale_tiles_a_slice(fmt) * 512; }
+
+struct GemmParams {
+    int64_t M, N, K;
+    int32_t slices;              // K slices, ceil(K / 256)
+    int32_t num_tm, num_tn;      // tiles along M and N
+    const float *xf;             // [M] row factors of x (kNv)
+    const float *wf;             // [N] row factors of w (kNv)
+    const uint16_t *bias;        // [N] BF16 or null
+    uint16_t *y;                 // [M, N] BF16
+    int32_t tma_y;               // y is stored by TMA (N a multiple of 8, y 16-byte aligned)
+};
+
+// Instruction descriptor of the block-scaled kinds, both operands E2M1 and K-major:
+//   bits 4-5 / 29-30 which byte of the scale words B / A use; bits 7-9 / 10-12 A / B format
+//   (1 = E2M1); bits 17-22 N >> 3; bit 23 scale type (0 = UE4M3, 1 = UE8M0); bits 27-28
+//   M >> 7.
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, int fmt, int sf)
+{
+    return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((fmt == kMx ? 1u : 0u) << 23) | (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(sf) << 29);
+}
+
+// One product step of 64 elements of K.  kMx: a scale word holds 4 scales of 32, a step
+// uses two of them (the descriptor says which); kNv: it uses all 4 scales of 16.
+template <int kFmt, int kCtas>
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate)
+{
+#define W8A8_FP4_MMA(group, kind)                                                          \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                         \
+                 "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d), \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate))
+    if constexpr (kFmt == kMx && kCtas == 1)
+        W8A8_FP4_MMA("1", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (kFmt == kMx)
+        W8A8_FP4_MMA("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (kCtas == 1)
+        W8A8_FP4_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else
+        W8A8_FP4_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+#undef W8A8_FP4_MMA
+}
+
+// 512-byte scale tile, shared -> tensor memory: 32 rows of 16 bytes to lanes 0-31 (and the
+// same to lanes 32-63, 64-95, 96-127) of 4 columns.  The descriptor: no swizzle, 8-row
+// groups 128 bytes apart.
+template <int kCtas>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
+                       (static_cast<uint64_t>(1u) << 46);
+    if constexpr (kCtas == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
+}
+
+// ------------------------------------------------------------------ pairs of CTAs
+// Tile 256 x 256, two CTAs of a cluster together (cta_group::2): each holds 128 rows of x and
+// 128 rows of w in shared memory and the accumulator of its 128 rows of y x all 256
+// columns in its tensor memory; the even CTA's MMA thread issues the products for both.
+// A slice then costs each SM 32 KB of codes and 4-6 KB of scales for 128 x 256 x 256
+// products.  One thread of each CTA loads its own half (signalling the even CTA's
+// barrier), four warps of each store their 128 rows.
+//
+// Tensor memory: two accumulators of 256 columns and the scales do not fit in 512 columns,
+// so the accumulators share columns: one at 0, the other ending where the scales begin.
+// The epilogue reads the shared columns first and then lets the next tile's products
+// start, so only that first read is not overlapped.
+constexpr int kPairStages = 5;
+constexpr int kPairThreads = 192;
+constexpr int kPairGroup = 8;                // M tiles of a raster group
+
+template <int kFmt>
+struct alignas(1024) PairSmem {
+    uint8_t a[kPairStages][128 * 128];
+    uint8_t b[kPairStages][128 * 128];
+    uint8_t sfa[kPairStages][scale_slice_bytes(kFmt)];
+    uint8_t sfb[kPairStages][2][scale_slice_bytes(kFmt)];
+    alignas(1024) uint8_t out[4][32 * 128];  // per epilogue warp: 32 rows x 64 BF16
+    float col[4][2][256];                    // per epilogue warp: row factors of w, bias
+    uint64_t full[kPairStages];              // both CTAs' bytes (the even CTA's)
+    uint64_t empty[kPairStages];
+    uint64_t tfull[2];
+    uint64_t tdrained;                       // shared columns read (the even CTA's)
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+template <int kFmt>
+constexpr size_t kPairSmemBytes = sizeof(PairSmem<kFmt>) + 1024;
+
+// Tensor memory columns of the pair kernel: SFA and SFB of one slice at the end.
+__host__ __device__ constexpr uint32_t pair_sf_cols(int fmt) { return 12u * scale_tiles_a_slice(fmt); }
+__host__ __device__ constexpr uint32_t pair_acc1(int fmt) { return 512u - pair_sf_cols(fmt) - 256u; }
+
+__device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// TMA load into this CTA's shared memory that signals a barrier of the pair's even CTA.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+                 : "memory");
+}
+// Arrives on the same barrier of both CTAs when this thread's products have completed.
+__device__ __forceinline__ void commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
+
+__device__ __forceinline__ void pair_tile(int t, const GemmParams &p, int &tm, int &tn)
+{
+    const int per_group = kPairGroup * p.num_tn;
+    const int group = t / per_group;
+    const int first = group * kPairGroup;
+    const int gsz = min(p.num_tm - first, kPairGroup);
+    const int local = t - group * per_group;
+    tm = first + local % gsz;
+    tn = local / gsz;
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmWs,
+                     const __grid_constant__ CUtensorMap tmY, const GemmParams p)
+{
+    constexpr int kTiles = scale_tiles_a_slice(kFmt);
+    constexpr uint32_t kSfBytes = scale_slice_bytes(kFmt);
+    constexpr uint32_t kSliceBytes = 2 * 128 * 128 + 3 * kSfBytes;
+    extern __shared__ uint8_t smem_raw[];
+    PairSmem<kFmt> &sm = *reinterpret_cast<PairSmem<kFmt> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                             ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const uint32_t rank = norm::cluster_rank();
+    volatile int *abort = &sm.abort;
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    const int num_tiles = p.num_tm * p.num_tn;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        mbar_init(&sm.tfull[0], 1);
+        mbar_init(&sm.tfull[1], 1);
+        mbar_init(&sm.tdrained, 8);
+        mbar_init(&sm.mma_done, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmXs);
+        prefetch_tensormap(&tmWs);
+        if (p.tma_y)
+            prefetch_tensormap(&tmY);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    norm::cluster_barrier();     // both CTAs' barriers are initialised and their TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    // The operands may come from the quantizer launched before: nothing below reads them
+    // before that grid has completed.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < num_tiles; t += pairs) {
+                int tm, tn;
+                pair_tile(t, p, tm, tn);
+                const int32_t row_x = tm * 256 + static_cast<int>(rank) * 128;
+                const int32_t row_w = tn * 256 + static_cast<int>(rank) * 128;
+                for (int ks = 0; ks < p.slices; ++ks, ++it) {
+                    const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1;
+                    if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&sm.full[s], 2 * kSliceBytes);
+                    const uint32_t bar = map_to(smem_u32(&sm.full[s]), 0);
+                    tma_load_pair(sm.a[s], &tmX, bar, ks * 128, row_x);
+                    tma_load_pair(sm.b[s], &tmW, bar, ks * 128, row_w);
+                    // scale maps count in 8-byte units: 64 a tile
+                    tma_load_pair(sm.sfa[s], &tmXs, bar, ks * (kTiles * 64), row_x >> 7);
+                    tma_load_pair(sm.sfb[s][0], &tmWs, bar, ks * (kTiles * 64), tn * 2);
+                    tma_load_pair(sm.sfb[s][1], &tmWs, bar, ks * (kTiles * 64), tn * 2 + 1);
+                }
+            }
+            if (!ok) {
+                // copies in flight land before shared memory is released: they need
+                // microseconds, the end of the kernel waits a millisecond for them
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull)
+                    ;
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (rank == 0 && lane == 0) {
+            const uint32_t sfa = tmem + 512 - pair_sf_cols(kFmt);
+            const uint32_t sfb = sfa + 4 * kTiles;
+            uint32_t it = 0, i = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < num_tiles; t += pairs, ++i) {
+                if (i > 0 && !gemm::gemm_wait(&sm.tdrained, (i - 1) & 1, abort))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem + (i & 1) * pair_acc1(kFmt);
+                for (int ks = 0; ks < p.slices; ++ks, ++it) {
+                    const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1;
+                    if (!gemm::gemm_wait(&sm.full[s], ph, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t fa = smem_u32(sm.sfa[s]), fb0 = smem_u32(sm.sfb[s][0]), fb1 = smem_u32(sm.sfb[s][1]);
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) {
+                        copy_scales<2>(sfa + 4 * j, fa + 512 * j);
+                        copy_scales<2>(sfb + 8 * j, fb0 + 512 * j);
+                        copy_scales<2>(sfb + 8 * j + 4, fb1 + 512 * j);
+                    }
+                    const uint64_t ad = umma_desc_sw128(smem_u32(sm.a[s]));
+                    const uint64_t bd = umma_desc_sw128(smem_u32(sm.b[s]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = kFmt == kMx ? k >> 1 : k;
+                        const uint32_t id = idesc_fp4(256, 256, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
+                        umma_fp4<kFmt, 2>(d, ad + 2 * k, bd + 2 * k, id, sfa + 4 * j, sfb + 8 * j, (ks | k) != 0);
+                    }
+                    commit_pair(&sm.empty[s]);
+                }
+                if (ok)
+                    commit_pair(&sm.tfull[i & 1]);
+            }
+            // every product issued here completes before tensor memory is released
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             smem_u32(&sm.mma_done))
+                         : "memory");
+            volatile int no_abort = 0;
+            mbar_wait(&sm.mma_done, 0, &no_abort, 100000000ull);
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        const int ew = warp - 2;
+        const int quarter = warp & 3;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t drained = map_to(smem_u32(&sm.tdrained), 0);
+        uint8_t *out = sm.out[ew];
+        float *wf = sm.col[ew][0], *bias = sm.col[ew][1];
+        uint32_t i = 0;
+        for (int t = pair; t < num_tiles; t += pairs, ++i) {
+            int tm, tn;
+            pair_tile(t, p, tm, tn);
+            const int64_t m_w = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32;
+            const int64_t m = m_w + lane;
+            const int64_t n0 = static_cast<int64_t>(tn) * 256;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t n = n0 + j * 32 + lane;
+                wf[j * 32 + lane] = kFmt == kNv && n < p.N ? __ldg(p.wf + n) : 1.0f;
+                bias[j * 32 + lane] =
+                    p.bias != nullptr && n < p.N ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16) : 0.0f;
+            }
+            const float xf = kFmt == kNv && m < p.M ? __ldg(p.xf + m) : 1.0f;
+            __syncwarp();
+            const uint32_t buf = i & 1;
+            if (!gemm::gemm_wait(&sm.tfull[buf], (i >> 1) & 1, abort))
+                break;
+            tc_fence_after();
+            const uint32_t acc = lane_base + buf * pair_acc1(kFmt);
+#pragma unroll 1
+            for (int step = 0; step < 4; ++step) {
+                // the 64 columns that hold the shared ones come first
+                const int c = buf == 0 ? 3 - step : step;
+                uint32_t r[2][32];
+                tmem_ld32(acc + c * 64, r[0]);
+                tmem_ld32(acc + c * 64 + 32, r[1]);
+                tmem_wait_ld(r[0]);
+                tmem_wait_ld(r[1]);
+                if (step == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_remote(drained);
+                }
+                if (lane == 0 && p.tma_y)
+                    gemm::tma_store_wait_read();
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int e = g * 8 + q * 2;
+                        const float2 f = *reinterpret_cast<const float2 *>(wf + c * 64 + e);
+                        const float2 b = *reinterpret_cast<const float2 *>(bias + c * 64 + e);
+                        const float v0 = __uint_as_float(r[e >> 5][e & 31]), v1 = __uint_as_float(r[e >> 5][(e & 31) + 1]);
+                        o[q] = kFmt == kNv ? pack_bf16x2(fmaf(v0, xf * f.x, b.x), fmaf(v1, xf * f.y, b.y))
+                                           : pack_bf16x2(v0 + b.x, v1 + b.y);
+                    }
+                    st_shared_v4(out + lane * 128 + ((g ^ (lane & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                }
+                const int64_t nc = n0 + c * 64;
+                if (p.tma_y) {
+                    gemm::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m_w < p.M && nc < p.N)
+                        gemm::tma_store_2d(&tmY, out, static_cast<int32_t>(nc), static_cast<int32_t>(m_w));
+                } else {
+                    __syncwarp();
+                    for (int rr = 0; rr < 32 && m_w + rr < p.M; ++rr) {
+                        uint16_t *dst = p.y + (m_w + rr) * p.N + nc;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int e = h * 32 + static_cast<int>(lane);
+                            if (nc + e < p.N)
+                                dst[e] = *reinterpret_cast<const uint16_t *>(out + rr * 128 + (((e >> 3) ^ (rr & 7)) << 4) +
+                                                                             (e & 7) * 2);
+                        }
+                    }
+                }
+            }
+        }
+        if (lane == 0 && p.tma_y)
+            gemm::tma_store_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // no CTA leaves while its peer may still read its shared memory or signal its barriers
+    norm::cluster_barrier();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// ------------------------------------------------------------------ few tokens
+// y^T: the weight's rows are the 128 rows of a product and BT tokens its columns, so that a
+// tile costs the weight's bytes and little else.  One tile a CTA; the K slices are split
+// over the S CTAs of a cluster, which add their FP32 partial tiles through distributed
+// shared memory in rank order (the result does not depend on timing).
+constexpr int kSkinnyThreads = 192;
+
+template <int kFmt, int BT>
+struct alignas(1024) SkinnySmem {
+    static constexpr int kStageBytes = 128 * 128 + BT * 128 + 2 * scale_slice_bytes(kFmt);
+    static constexpr int kStages = 204800 / kStageBytes < 8 ? 204800 / kStageBytes : 8;
+    uint8_t w[kStages][128 * 128];       // after the last product: partial [BT][128] FP32
+    uint8_t x[kStages][BT * 128];
+    uint8_t sfw[kStages][scale_slice_bytes(kFmt)];
+    uint8_t sfx[kStages][scale_slice_bytes(kFmt)];
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t tfull;
+    uint32_t tmem_base;
+    int abort;
+    static_assert(BT * 128 * 4 <= kStages * 128 * 128, "partial tile does not fit");
+};
+template <int kFmt, int BT>
+constexpr size_t kSkinnySmemBytes = sizeof(SkinnySmem<kFmt, BT>) + 1024;
+
+template <int kFmt, int BT>
+__global__ void __launch_bounds__(kSkinnyThreads, 1)
+    gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmWs,
+                       const GemmParams p)
+{
+    using S = SkinnySmem<kFmt, BT>;
+    constexpr int kTiles = scale_tiles_a_slice(kFmt);
+    constexpr int kStages = S::kStages;
+    constexpr uint32_t kCols = BT + 8 * kTiles <= 64 ? 64 : (BT + 8 * kTiles <= 128 ? 128 : 256);
+    extern __shared__ uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const int rank = static_cast<int>(norm::cluster_rank()), splits = static_cast<int>(norm::cluster_size());
+    volatile int *abort = &sm.abort;
+    const int tile = static_cast<int>(blockIdx.x) / splits;
+    const int tn = tile % p.num_tn, tm = tile / p.num_tn;
+    // the rank's slices
+    const int ks0 = static_cast<int>(static_cast<int64_t>(p.slices) * rank / splits);
+    const int ks1 = static_cast<int>(static_cast<int64_t>(p.slices) * (rank + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        mbar_init(&sm.tfull, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmXs);
+        prefetch_tensormap(&tmWs);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.full[s], S::kStageBytes);
+                tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
+                tma_load_2d(sm.sfw[s], &tmWs, &sm.full[s], ks * (kTiles * 64), tn);
+                tma_load_2d(sm.x[s], &tmX, &sm.full[s], ks * 128, tm * BT);
+                tma_load_2d(sm.sfx[s], &tmXs, &sm.full[s], ks * (kTiles * 64), tm * BT / 128);
+            }
+            if (!ok) {
+                volatile int no_abort = 0;
+                const uint32_t first = it > kStages ? it - kStages : 0;
+                for (uint32_t j = first; j < it; ++j)
+                    mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, &no_abort, 100000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t sfw = tmem + BT, sfx = sfw + 4 * kTiles;
+            uint32_t it = 0;
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                if (!gemm::gemm_wait(&sm.full[s], ph, abort))
+                    break;
+                tc_fence_after();
+                const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    copy_scales<1>(sfw + 4 * j, fw + 512 * j);
+                    copy_scales<1>(sfx + 4 * j, fx + 512 * j);
+                }
+                const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
+                const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = kFmt == kMx ? k >> 1 : k;
+                    const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
+                    umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
+                }
+                umma_commit(&sm.empty[s]);
+            }
+            umma_commit(&sm.tfull);
+        }
+    }
+    float *part = reinterpret_cast<float *>(sm.w);
+    if (warp >= 2) {
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + static_cast<int>(lane);
+        const int64_t n = static_cast<int64_t>(tn) * 128 + row;
+        const bool ok = gemm::gemm_wait(&sm.tfull, 0, abort);
+        tc_fence_after();
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        if (ok) {
+#pragma unroll
+            for (int c = 0; c < BT; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(acc + c, r);
+                tmem_wait_ld(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    part[(c + i) * 128 + row] = __uint_as_float(r[i]);
+            }
+        }
+        (void)n;
+    }
+    tc_fence_before();
+    __syncthreads();
+    norm::cluster_barrier();     // every rank's partial tile is in its shared memory
+    if (warp >= 2 && !*abort) {
+        const int row = static_cast<int>(threadIdx.x) - 64;
+        const int64_t n = static_cast<int64_t>(tn) * 128 + row;
+        if (n < p.N) {
+            const float wf = kFmt == kNv ? __ldg(p.wf + n) : 1.0f;
+            const float b = p.bias != nullptr ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16) : 0.0f;
+            for (int t = rank; t < BT && static_cast<int64_t>(tm) * BT + t < p.M; t += splits) {
+                const int64_t m = static_cast<int64_t>(tm) * BT + t;
+                float v = 0.0f;
+                for (int q = 0; q < splits; ++q) {
+                    float u;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u)
+                                 : "r"(map_to(smem_u32(part + t * 128 + row), static_cast<uint32_t>(q))));
+                    v += u;
+                }
+                v = kFmt == kNv ? fmaf(v, __ldg(p.xf + m) * wf, b) : v + b;
+                p.y[m * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+            }
+        }
+    }
+    norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
+    if (warp == 1)
+        tmem_dealloc(tmem, kCols);
+}
+
+} // namespace fp4
+} // namespace w8a8

@@ -1,0 +1,321 @@
+// fp4_host.cuh -- host side of the 4-bit linear and of the fused block norm: choice of
+// variant, tensor maps and launches.  Included by w8a8.cu inside its unnamed namespace,
+// after the helpers it shares (device table, pointer checks, make_map).
+
+// ------------------------------------------------------------------ sizes and checks
+bool fp4_format_ok(int format) { return format == W8A8_FP4_MX || format == W8A8_FP4_NV; }
+
+size_t fp4_scale_bytes(int64_t rows, int64_t K, int format)
+{
+    return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(fp4::scale_tiles(K, format)) * 512;
+}
+
+// Quantized matrix in device memory: every buffer present, on this device and aligned.
+w8a8_status_t check_fp4(const void *codes, const void *scales, const void *factor, int format)
+{
+    W8A8_TRY(check_device_ptr(codes));
+    W8A8_TRY(check_device_ptr(scales));
+    if (format == W8A8_FP4_NV)
+        W8A8_TRY(check_device_ptr(factor));
+    else if (factor != nullptr)
+        return W8A8_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || (reinterpret_cast<uintptr_t>(factor) & 3u))
+        return W8A8_ERR_ALIGNMENT;
+    return W8A8_OK;
+}
+
+w8a8_status_t fp4_shape(int64_t rows, int64_t K)
+{
+    if (rows < 0 || K < 0)
+        return W8A8_ERR_INVALID_ARG;
+    if (K == 0 || K % 32 || rows > kMaxTmaCoord || K > kMaxTmaCoord)
+        return W8A8_ERR_SHAPE;
+    return W8A8_OK;
+}
+
+// ------------------------------------------------------------------ quantizer
+// W warps a row, P pieces of 16 values a lane.
+template <int kFmt, int W, int P>
+w8a8_status_t launch_fp4_quantize_t(const fp4::QParams &p, cudaStream_t stream)
+{
+    constexpr int rows = fp4::kWarps / W;
+    const int64_t grid = (p.rows_pad + rows - 1) / rows;
+    fp4::quantize_kernel<kFmt, W, P><<<static_cast<unsigned>(grid), fp4::kWarps * 32, 0, stream>>>(p);
+    return launch_status();
+}
+
+template <int kFmt, int P>
+w8a8_status_t launch_fp4_quantize_p(const fp4::QParams &p, cudaStream_t stream)
+{
+    const int64_t pieces = p.K / 16;
+    if (pieces <= 32 * P)
+        return launch_fp4_quantize_t<kFmt, 1, P>(p, stream);
+    if (pieces <= 64 * P)
+        return launch_fp4_quantize_t<kFmt, 2, P>(p, stream);
+    if (pieces <= 128 * P)
+        return launch_fp4_quantize_t<kFmt, 4, P>(p, stream);
+    return launch_fp4_quantize_t<kFmt, 8, P>(p, stream);
+}
+
+w8a8_status_t launch_fp4_quantize(const uint16_t *x, int64_t rows, int64_t K, int format, uint8_t *codes,
+                                  uint8_t *scales, float *factor, cudaStream_t stream)
+{
+    int dev;
+    W8A8_TRY(current_device(dev));
+    fp4::QParams p{};
+    p.x = x;
+    p.rows = rows;
+    p.rows_pad = (rows + 127) / 128 * 128;
+    p.K = K;
+    p.codes = codes;
+    p.scales = scales;
+    p.factor = factor;
+    const bool spread = rows < 8 * g_dev[dev].sms && K <= 16 * 32 * fp4::kWarps;
+    if (format == W8A8_FP4_MX)
+        return spread ? launch_fp4_quantize_p<fp4::kMx, 1>(p, stream) : launch_fp4_quantize_p<fp4::kMx, 4>(p, stream);
+    return spread ? launch_fp4_quantize_p<fp4::kNv, 1>(p, stream) : launch_fp4_quantize_p<fp4::kNv, 4>(p, stream);
+}
+
+// ------------------------------------------------------------------ product
+w8a8_status_t fp4_maps(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int format,
+                       uint32_t box_rows, CUtensorMap &mc, CUtensorMap &ms)
+{
+    W8A8_TRY(make_map(mc, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, K / 2, box_rows, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B));
+    // scale tiles of a row of tiles are contiguous: 8-byte units, 64 a tile
+    return make_map(ms, scales, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 8, (rows + 127) / 128,
+                    fp4::scale_tiles(K, format) * 64, 1, static_cast<uint32_t>(fp4::scale_tiles_a_slice(format) * 64),
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+struct Fp4Operand {
+    const uint8_t *codes, *scales;
+    const float *factor;
+};
+
+template <int kFmt>
+w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream, bool pdl)
+{
+    int dev;
+    W8A8_TRY(current_device(dev));
+    CUtensorMap mx, mxs, mw, mws, my;
+    W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, 128, mx, mxs));
+    W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 128, mw, mws));
+    p.tma_y = p.N % 8 == 0 && aligned16(p.y);
+    my = mx;
+    if (p.tma_y)
+        W8A8_TRY(make_map(my, p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.M, p.N, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
+    p.num_tm = static_cast<int32_t>((p.M + 255) / 256);
+    p.num_tn = static_cast<int32_t>((p.N + 255) / 256);
+    if (static_cast<int64_t>(p.num_tm) * p.num_tn >= (int64_t{1} << 30))
+        return W8A8_ERR_SHAPE;
+    auto kern = fp4::gemm_pair_kernel<kFmt>;
+    constexpr size_t smem = fp4::kPairSmemBytes<kFmt>;
+    static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(fp4::kPairThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int pairs;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        int &known = g_dev[dev].fp4_pairs[kFmt];
+        if (known == 0) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(smem));
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+            int n = 0;
+            cfg.gridDim = dim3(static_cast<unsigned>(g_dev[dev].sms / 2 * 2));
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+                cudaGetLastError();
+                n = g_dev[dev].sms / 2;
+            }
+            known = n;
+        }
+        pairs = known;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, p.num_tm * p.num_tn)));
+    cfg.numAttrs = pdl ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, my, p);
+    return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+template <int kFmt, int BT>
+w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream, bool pdl)
+{
+    int dev;
+    W8A8_TRY(current_device(dev));
+    CUtensorMap mx, mxs, mw, mws;
+    W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, BT, mx, mxs));
+    W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 128, mw, mws));
+    p.num_tm = static_cast<int32_t>((p.M + BT - 1) / BT);
+    p.num_tn = static_cast<int32_t>((p.N + 127) / 128);
+    const int64_t tiles = static_cast<int64_t>(p.num_tm) * p.num_tn;
+    if (tiles >= (int64_t{1} << 27))
+        return W8A8_ERR_SHAPE;
+    auto kern = fp4::gemm_skinny_kernel<kFmt, BT>;
+    constexpr size_t smem = fp4::kSkinnySmemBytes<kFmt, BT>;
+    static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
+    constexpr int slot = kFmt * 4 + (BT == 16 ? 0 : BT == 32 ? 1 : BT == 64 ? 2 : 3);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_dev[dev].fp4_skinny_attr_set[slot]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(smem));
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+            g_dev[dev].fp4_skinny_attr_set[slot] = true;
+        }
+    }
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= g_dev[dev].sms && splits * 2 <= p.slices)
+        splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(fp4::kSkinnyThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, p);
+    return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+template <int kFmt>
+w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const fp4::GemmParams &p, cudaStream_t stream,
+                                bool pdl)
+{
+    if (p.M <= 16)
+        return launch_fp4_skinny<kFmt, 16>(x, w, p, stream, pdl);
+    if (p.M <= 32)
+        return launch_fp4_skinny<kFmt, 32>(x, w, p, stream, pdl);
+    if (p.M <= 64)
+        return launch_fp4_skinny<kFmt, 64>(x, w, p, stream, pdl);
+    if (p.M <= 128)
+        return launch_fp4_skinny<kFmt, 128>(x, w, p, stream, pdl);
+    return launch_fp4_pair<kFmt>(x, w, p, stream, pdl);
+}
+
+w8a8_status_t launch_fp4_gemm(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
+                              const uint16_t *bias, uint16_t *y, cudaStream_t stream, bool pdl)
+{
+    fp4::GemmParams p{};
+    p.M = M;
+    p.N = w->N;
+    p.K = K;
+    p.slices = static_cast<int32_t>((K + fp4::kSliceK - 1) / fp4::kSliceK);
+    p.xf = x.factor;
+    p.wf = w->factor;
+    p.bias = bias;
+    p.y = y;
+    const Fp4Operand wo{w->codes, w->scales, w->factor};
+    return w->format == W8A8_FP4_MX ? launch_fp4_gemm_t<fp4::kMx>(x, wo, p, stream, pdl)
+                                    : launch_fp4_gemm_t<fp4::kNv>(x, wo, p, stream, pdl);
+}
+
+// A weight record: consistent fields; the buffers are checked by whoever uses them.
+w8a8_status_t check_fp4_weight(const w8a8_fp4_weight_t *w, int64_t K)
+{
+    if (w == nullptr || w->N < 0 || w->K != K || !fp4_format_ok(w->format))
+        return W8A8_ERR_INVALID_ARG;
+    if ((w->codes == nullptr) != (w->scales == nullptr))
+        return W8A8_ERR_INVALID_ARG;
+    if (w->codes == nullptr && w->w_bf16 == nullptr)
+        return W8A8_ERR_INVALID_ARG;
+    return W8A8_OK;
+}
+
+// ------------------------------------------------------------------ block norm
+template <int kOut, int V, int W, int P, bool kLong>
+w8a8_status_t launch_block_norm_t(const bnorm::Params &p, cudaStream_t stream)
+{
+    constexpr int rows = bnorm::kWarps / W;
+    const int64_t total = kOut == bnorm::kOutBf16 ? p.M : p.M_pad;
+    const int64_t grid = (total + rows - 1) / rows;
+    bnorm::block_norm_kernel<kOut, V, W, P, kLong>
+        <<<static_cast<unsigned>(grid), bnorm::kWarps * 32, 0, stream>>>(p);
+    return launch_status();
+}
+
+// The fewest warps that hold a row with one piece of 16 values a lane, then more pieces.
+template <int kOut, int V>
+w8a8_status_t launch_block_norm_v(const bnorm::Params &p, cudaStream_t stream)
+{
+    constexpr int Q = 16 / V;
+    const int64_t k = p.K;
+    if (k <= 512)
+        return launch_block_norm_t<kOut, V, 1, Q, false>(p, stream);
+    if (k <= 1024)
+        return launch_block_norm_t<kOut, V, 2, Q, false>(p, stream);
+    if (k <= 2048)
+        return launch_block_norm_t<kOut, V, 4, Q, false>(p, stream);
+    if (k <= 4096)
+        return launch_block_norm_t<kOut, V, 8, Q, false>(p, stream);
+    if (k <= 8192)
+        return launch_block_norm_t<kOut, V, 8, 2 * Q, false>(p, stream);
+    if (k <= 16384)
+        return launch_block_norm_t<kOut, V, 8, 4 * Q, false>(p, stream);
+    return launch_block_norm_t<kOut, V, 8, 2 * Q, true>(p, stream);
+}
+
+// Arguments that both forms share -> p.
+w8a8_status_t block_norm_common(const uint16_t *h, const uint16_t *y, int post_norm, const uint16_t *post_gamma,
+                                const uint16_t *gate, float res_scale, const uint16_t *pre_gamma,
+                                const uint16_t *scale, const uint16_t *shift, int64_t T, float eps, int64_t M,
+                                int64_t K, uint16_t *h_out, bnorm::Params &p)
+{
+    if (M < 0 || K < 0 || T <= 0 || !(eps >= 0.0f) || !(eps <= 3.4e38f) || !(res_scale >= -3.4e38f) ||
+        !(res_scale <= 3.4e38f) || (post_gamma != nullptr && !post_norm))
+        return W8A8_ERR_INVALID_ARG;
+    if (K == 0 || K % 8 || M % T || M > kMaxTmaCoord || K > kMaxTmaCoord)
+        return W8A8_ERR_SHAPE;
+    if (M == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_device_ptr(h));
+    W8A8_TRY(check_device_ptr(y));
+    W8A8_TRY(check_device_ptr(h_out));
+    const uint16_t *columns[5] = {post_gamma, gate, pre_gamma, scale, shift};
+    for (const uint16_t *c : columns) {
+        if (c == nullptr)
+            continue;
+        W8A8_TRY(check_device_ptr(c));
+        if (!aligned16(c))
+            return W8A8_ERR_ALIGNMENT;
+    }
+    if (!aligned16(h) || !aligned16(y) || !aligned16(h_out))
+        return W8A8_ERR_ALIGNMENT;
+    p = bnorm::Params{};
+    p.h = h;
+    p.y = y;
+    p.post_gamma = post_gamma;
+    p.pre_gamma = pre_gamma;
+    p.gate = gate;
+    p.scale = scale;
+    p.shift = shift;
+    p.M = M;
+    p.M_pad = (M + 127) / 128 * 128;
+    p.K = K;
+    p.T = T;
+    p.eps = eps;
+    p.res_scale = res_scale;
+    p.post_norm = post_norm;
+    p.h_out = h_out;
+    return W8A8_OK;
+}

@@ -9,7 +9,10 @@
 #include <mutex>
 
 #include "../../include/w8a8.h"
+#include "block_norm.cuh"
 #include "common.cuh"
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
 #include "gemm.cuh"
 #include "norm.cuh"
 #include "quant.cuh"
@@ -32,6 +35,8 @@ struct DeviceInfo {
     bool rstd_attr_set = false;
     bool norm_attr_set[4] = {false, false, false, false};
     int norm_max_clusters[norm::kMaxCluster + 1] = {};    // by cluster size, 0 = unknown
+    int fp4_pairs[2] = {0, 0};                             // by format: pairs that fit, 0 = unknown
+    bool fp4_skinny_attr_set[8] = {};                      // by format and token tile
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -609,6 +614,8 @@ w8a8_status_t host_pipe(int dev, HostPipe *&hp)
     return W8A8_OK;
 }
 
+#include "fp4_host.cuh"
+
 } // namespace
 
 extern "C" {
@@ -1014,6 +1021,173 @@ w8a8_status_t w8a8_rowwise_linear(const int8_t *xq, const float *xs, int64_t M, 
     p.bias = bias;
     p.y = y;
     return launch_gemm<gemm::Mode::kI8Row>(xq, wq, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t w8a8_fp4_scale_bytes(int64_t rows, int64_t K, int format)
+{
+    if (rows <= 0 || K <= 0 || K % 32 || !fp4_format_ok(format))
+        return 0;
+    return fp4_scale_bytes(rows, K, format);
+}
+
+w8a8_status_t w8a8_fp4_quantize(const w8a8_bf16_t *x, int64_t rows, int64_t K, int format,
+                                uint8_t *codes, uint8_t *scales, float *factor, void *stream)
+{
+    if (!fp4_format_ok(format))
+        return W8A8_ERR_INVALID_ARG;
+    W8A8_TRY(fp4_shape(rows, K));
+    if (rows == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_device_ptr(x));
+    W8A8_TRY(check_fp4(codes, scales, factor, format));
+    if (!aligned16(x))
+        return W8A8_ERR_ALIGNMENT;
+    return launch_fp4_quantize(x, rows, K, format, codes, scales, factor, static_cast<cudaStream_t>(stream));
+}
+
+w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, const float *factor,
+                                  int64_t rows, int64_t K, int format, w8a8_bf16_t *y,
+                                  void *stream)
+{
+    if (!fp4_format_ok(format))
+        return W8A8_ERR_INVALID_ARG;
+    W8A8_TRY(fp4_shape(rows, K));
+    if (rows == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_fp4(codes, scales, factor, format));
+    W8A8_TRY(check_device_ptr(y));
+    if (!aligned16(y))
+        return W8A8_ERR_ALIGNMENT;
+    const fp4::DParams p{codes, scales, factor, rows, K, y};
+    const int64_t grid = (rows * ((K / 16 + 31) / 32) + fp4::kWarps - 1) / fp4::kWarps;
+    if (grid > 0x7FFFFFFF)
+        return W8A8_ERR_SHAPE;
+    auto kern = format == W8A8_FP4_MX ? fp4::dequantize_kernel<fp4::kMx> : fp4::dequantize_kernel<fp4::kNv>;
+    kern<<<static_cast<unsigned>(grid), fp4::kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launch_status();
+}
+
+size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format)
+{
+    if (M <= 0 || K <= 0 || K % 32 || !fp4_format_ok(format))
+        return 0;
+    return round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2)) + fp4_scale_bytes(M, K, format) +
+           (format == W8A8_FP4_NV ? static_cast<size_t>(M) * sizeof(float) : 0);
+}
+
+w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
+                              const w8a8_fp4_weight_t *w, const w8a8_bf16_t *bias, w8a8_bf16_t *y,
+                              void *workspace, size_t workspace_bytes, int *path_taken,
+                              void *stream)
+{
+    if (path_taken != nullptr)
+        *path_taken = W8A8_PATH_NONE;
+    if (M < 0 || K < 0)
+        return W8A8_ERR_INVALID_ARG;
+    W8A8_TRY(check_fp4_weight(w, K));
+    const int64_t N = w->N;
+    if (M == 0 || N == 0)
+        return W8A8_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K > 0)
+        W8A8_TRY(check_device_ptr(x));
+    W8A8_TRY(check_device_ptr(y));
+    if (bias != nullptr)
+        W8A8_TRY(check_device_ptr(bias));
+    const bool four = K > 0 && K % 32 == 0 && K <= kMaxTmaCoord && M <= kMaxTmaCoord && N <= kMaxTmaCoord &&
+                      w->codes != nullptr && aligned16(x);
+    if (!four) {
+        if (w->w_bf16 == nullptr)
+            return K > 0 && K % 32 == 0 && !aligned16(x) ? W8A8_ERR_ALIGNMENT : W8A8_ERR_SHAPE;
+        if (K > 0)
+            W8A8_TRY(check_device_ptr(w->w_bf16));
+        W8A8_TRY(bf16_impl(x, w->w_bf16, bias, y, M, K, N, st));
+        if (path_taken != nullptr)
+            *path_taken = W8A8_PATH_BF16;
+        return W8A8_OK;
+    }
+    W8A8_TRY(check_fp4(w->codes, w->scales, w->factor, w->format));
+    if (workspace == nullptr || !aligned16(workspace) ||
+        workspace_bytes < w8a8_fp4_linear_workspace_bytes(M, K, w->format))
+        return W8A8_ERR_WORKSPACE;
+    W8A8_TRY(check_device_ptr(workspace));
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2));
+    float *factor = w->format == W8A8_FP4_NV
+                        ? reinterpret_cast<float *>(scales + fp4_scale_bytes(M, K, w->format))
+                        : nullptr;
+    W8A8_TRY(launch_fp4_quantize(x, M, K, w->format, codes, scales, factor, st));
+    W8A8_TRY(launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, st, true));
+    if (path_taken != nullptr)
+        *path_taken = W8A8_PATH_FP4;
+    return W8A8_OK;
+}
+
+w8a8_status_t w8a8_fp4_linear_prequant(const uint8_t *codes, const uint8_t *scales,
+                                       const float *factor, int64_t M, int64_t K,
+                                       const w8a8_fp4_weight_t *w, const w8a8_bf16_t *bias,
+                                       w8a8_bf16_t *y, void *stream)
+{
+    W8A8_TRY(check_fp4_weight(w, K));
+    if (w->codes == nullptr)
+        return W8A8_ERR_INVALID_ARG;
+    W8A8_TRY(fp4_shape(M, K));
+    W8A8_TRY(fp4_shape(w->N, K));
+    if (M == 0 || w->N == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_fp4(codes, scales, factor, w->format));
+    W8A8_TRY(check_fp4(w->codes, w->scales, w->factor, w->format));
+    W8A8_TRY(check_device_ptr(y));
+    if (bias != nullptr)
+        W8A8_TRY(check_device_ptr(bias));
+    return launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, static_cast<cudaStream_t>(stream),
+                           false);
+}
+
+w8a8_status_t w8a8_block_norm(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,
+                              const w8a8_bf16_t *post_gamma, const w8a8_bf16_t *gate,
+                              float res_scale, const w8a8_bf16_t *pre_gamma,
+                              const w8a8_bf16_t *scale, const w8a8_bf16_t *shift, int64_t T,
+                              float eps, int64_t M, int64_t K, w8a8_bf16_t *h_out,
+                              w8a8_bf16_t *n_out, void *stream)
+{
+    bnorm::Params p;
+    W8A8_TRY(block_norm_common(h, y, post_norm, post_gamma, gate, res_scale, pre_gamma, scale, shift, T, eps, M, K,
+                               h_out, p));
+    if (M == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_device_ptr(n_out));
+    if (!aligned16(n_out))
+        return W8A8_ERR_ALIGNMENT;
+    p.n_out = n_out;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // 16 values a lane wherever 4-bit output exists too, so that both forms add a row's
+    // squares in the same order and give the same bits
+    return K % 32 == 0 ? launch_block_norm_v<bnorm::kOutBf16, 16>(p, st) : launch_block_norm_v<bnorm::kOutBf16, 8>(p, st);
+}
+
+w8a8_status_t w8a8_block_norm_fp4(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,
+                                  const w8a8_bf16_t *post_gamma, const w8a8_bf16_t *gate,
+                                  float res_scale, const w8a8_bf16_t *pre_gamma,
+                                  const w8a8_bf16_t *scale, const w8a8_bf16_t *shift, int64_t T,
+                                  float eps, int64_t M, int64_t K, int format, w8a8_bf16_t *h_out,
+                                  uint8_t *codes, uint8_t *scales, float *factor, void *stream)
+{
+    if (!fp4_format_ok(format))
+        return W8A8_ERR_INVALID_ARG;
+    bnorm::Params p;
+    W8A8_TRY(block_norm_common(h, y, post_norm, post_gamma, gate, res_scale, pre_gamma, scale, shift, T, eps, M, K,
+                               h_out, p));
+    if (K % 32)
+        return W8A8_ERR_SHAPE;
+    if (M == 0)
+        return W8A8_OK;
+    W8A8_TRY(check_fp4(codes, scales, factor, format));
+    p.codes = codes;
+    p.scales = scales;
+    p.factor = factor;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return format == W8A8_FP4_MX ? launch_block_norm_v<fp4::kMx, 16>(p, st) : launch_block_norm_v<fp4::kNv, 16>(p, st);
 }
 
 w8a8_status_t w8a8_debug_block_sums(const int8_t *xq, const int8_t *wq, int64_t M, int64_t K,

@@ -69,7 +69,8 @@ typedef enum {
 typedef enum {
     W8A8_PATH_INT8 = 0,         /* quantize activations + INT8 block-scaled GEMM       */
     W8A8_PATH_BF16 = 1,         /* guard rejected the shape: BF16 GEMM                 */
-    W8A8_PATH_NONE = 2          /* nothing to compute (M == 0 or N == 0)               */
+    W8A8_PATH_NONE = 2,         /* nothing to compute (M == 0 or N == 0)               */
+    W8A8_PATH_FP4 = 3           /* quantize activations + block-scaled 4-bit GEMM      */
 } w8a8_path_t;
 
 /* Device-side error codes read by w8a8_device_error(). */
@@ -300,6 +301,119 @@ W8A8_API w8a8_status_t w8a8_rowwise_quantize(const w8a8_bf16_t *x, int64_t rows,
 W8A8_API w8a8_status_t w8a8_rowwise_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K,
                                            const int8_t *wq, const float *ws, int64_t N,
                                            const w8a8_bf16_t *bias, w8a8_bf16_t *y,
+                                           void *stream);
+
+/* ---- The microscaled 4-bit linear ----------------------------------------------------
+ * The same layer with both operands in 4-bit floating point (E2M1: 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives) and one scale per block along K, which the tensor cores apply
+ * themselves.  Not on the pages; the next step down from the INT8 operators above.
+ *
+ * Formats, for a row v of K values:
+ *   W8A8_FP4_MX  blocks of 32, scale 2^e, e = max(floor(log2 max|block|) - 2, -127), stored
+ *                as the byte e + 127 (0 for a zero block); code = e2m1(v 2^-e).
+ *   W8A8_FP4_NV  blocks of 16 with an E4M3 scale s, and an FP32 factor per row:
+ *                A = max(max|row|, 2^-100), factor = fl32(A / 2688),
+ *                s = e4m3(448 max|block| / A), code = e2m1(2688 v / (s A)), 0 where s = 0.
+ *   e2m1 and e4m3 round to nearest even and saturate; the quotients are rounded as if
+ *   exact.  A value is code * scale (* factor).  Infinities and NaN: the block's scale is
+ *   NaN (MX), the row's factor is NaN (NV), their codes 0.
+ *
+ * Layout of a quantized matrix [rows, K], K a positive multiple of 32:
+ *   codes  [rows, K/2] bytes, element 2 i in the low half of byte i;
+ *   scales w8a8_fp4_scale_bytes(rows, K, format) bytes: 512-byte tiles of 128 rows x 4 blocks,
+ *          tile (row / 128, block / 4) of [ceil(rows/128), ceil(blocks/4)], byte
+ *          16 (row % 32) + 4 (row % 128 / 32) + block % 4.  The bytes of blocks past the end
+ *          of K must be 0 (the quantizer writes 0 there and in rows past the end);
+ *   factor [rows] FP32 (NV), NULL (MX).
+ * codes and scales 16-byte aligned, factor 4-byte aligned. */
+typedef enum {
+    W8A8_FP4_MX = 0,
+    W8A8_FP4_NV = 1
+} w8a8_fp4_format_t;
+
+/* A weight [N, K] in 4 bits.  codes, scales, factor as above (factor NULL for MX); w_bf16:
+ * [N, K] BF16, NULL if the caller keeps no copy for the guard's fallback.  codes and scales
+ * may both be NULL if K is not a multiple of 32 (the layer then always takes BF16). */
+typedef struct {
+    int64_t N;
+    int64_t K;
+    int32_t format;             /* w8a8_fp4_format_t */
+    const w8a8_bf16_t *w_bf16;
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const float *factor;
+} w8a8_fp4_weight_t;
+
+/* Bytes of a quantized matrix's scales; 0 for sizes that cannot be quantized. */
+W8A8_API size_t w8a8_fp4_scale_bytes(int64_t rows, int64_t K, int format);
+
+/* x [rows, K] BF16 -> codes, scales, factor (activations on every call, weights once).
+ *   K a positive multiple of 32 (else W8A8_ERR_SHAPE); any rows >= 0; x 16-byte aligned.
+ *   A row's result depends on that row alone. */
+W8A8_API w8a8_status_t w8a8_fp4_quantize(const w8a8_bf16_t *x, int64_t rows, int64_t K, int format,
+                                         uint8_t *codes, uint8_t *scales, float *factor,
+                                         void *stream);
+
+/* The values that the codes stand for, y [rows, K] BF16 (16-byte aligned): code * scale is
+ * exact, its product with the factor is rounded to FP32 and then to BF16. */
+W8A8_API w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales,
+                                           const float *factor, int64_t rows, int64_t K, int format,
+                                           w8a8_bf16_t *y, void *stream);
+
+/* Bytes of device workspace of w8a8_fp4_linear: the quantized activations.  0 when K is not
+ * a positive multiple of 32 (the BF16 path) or M is 0. */
+W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format);
+
+/* Y[M, N] = X[M, K] W^T + bias with X quantized in the call to the weight's format:
+ *     y[m,n] = bf16( factor_x[m] factor_w[n] * sum_k value_x[m,k] value_w[n,k] + bias[n] ),
+ *   values without factors, FP32 accumulation, one rounding to BF16; the sum's order is fixed
+ *   by M, N and K.  Guard: the 4-bit path runs iff K is a positive multiple of 32, the weight
+ *   has codes and x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and
+ *   without that copy the call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M
+ *   and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,
+ *   else W8A8_ERR_WORKSPACE; may be NULL on the BF16 path.  path_taken as for w8a8_linear. */
+W8A8_API w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
+                                       const w8a8_fp4_weight_t *w, const w8a8_bf16_t *bias,
+                                       w8a8_bf16_t *y, void *workspace, size_t workspace_bytes,
+                                       int *path_taken, void *stream);
+
+/* The product alone, on activations already quantized to the weight's format (factor NULL
+ * for MX).  Any M and N; K a positive multiple of 32 (else W8A8_ERR_SHAPE). */
+W8A8_API w8a8_status_t w8a8_fp4_linear_prequant(const uint8_t *codes, const uint8_t *scales,
+                                                const float *factor, int64_t M, int64_t K,
+                                                const w8a8_fp4_weight_t *w,
+                                                const w8a8_bf16_t *bias, w8a8_bf16_t *y,
+                                                void *stream);
+
+/* ---- The residual update between two blocks ------------------------------------------
+ * A branch's output y joins the residual stream h through its own RMSNorm (post-norm), gate
+ * and residual scale, and the next branch's normalised input is formed in the same pass:
+ *     u       = y, or with post_norm != 0  (y * rstd(y)) (* post_gamma)
+ *     h'[m,k] = bf16( res_scale * h[m,k] + (gate[m/T,k] *) u[m,k] )
+ *     n[m,k]  = bf16( ((h' * rstd(h')) (* pre_gamma[k])) (* (1 + scale[m/T,k])) (+ shift[m/T,k]) )
+ *     rstd(v)[m] = 1 / sqrt( mean_k v[m,k]^2 + eps )
+ *   all in FP32 (statistics included), rounded at h' and n only.  post_gamma, pre_gamma [K]
+ *   and gate, scale, shift [M/T, K] BF16, each NULL to leave its factor out (post_gamma
+ *   needs post_norm).  h, y [M, K]; h_out [M, K] may be h itself, no other overlap.  K a
+ *   positive multiple of 8, T > 0 dividing M (else W8A8_ERR_SHAPE; T <= 0 gives
+ *   W8A8_ERR_INVALID_ARG), eps >= 0 and finite, res_scale finite; all buffers 16-byte
+ *   aligned.  A row of zeros with eps = 0 gives NaN, as the formula does. */
+W8A8_API w8a8_status_t w8a8_block_norm(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,
+                                       const w8a8_bf16_t *post_gamma, const w8a8_bf16_t *gate,
+                                       float res_scale, const w8a8_bf16_t *pre_gamma,
+                                       const w8a8_bf16_t *scale, const w8a8_bf16_t *shift,
+                                       int64_t T, float eps, int64_t M, int64_t K,
+                                       w8a8_bf16_t *h_out, w8a8_bf16_t *n_out, void *stream);
+
+/* w8a8_block_norm with n quantized as by w8a8_fp4_quantize instead of stored (the same bits
+ * as the two calls).  K a positive multiple of 32 (else W8A8_ERR_SHAPE). */
+W8A8_API w8a8_status_t w8a8_block_norm_fp4(const w8a8_bf16_t *h, const w8a8_bf16_t *y,
+                                           int post_norm, const w8a8_bf16_t *post_gamma,
+                                           const w8a8_bf16_t *gate, float res_scale,
+                                           const w8a8_bf16_t *pre_gamma, const w8a8_bf16_t *scale,
+                                           const w8a8_bf16_t *shift, int64_t T, float eps,
+                                           int64_t M, int64_t K, int format, w8a8_bf16_t *h_out,
+                                           uint8_t *codes, uint8_t *scales, float *factor,
                                            void *stream);
 
 /* Test hook: the INT32 partial products P[m, n, kb] = sum over the 128 k of K block kb of

@@ -237,7 +237,7 @@ w8a8_status_t check_fp4_weight(const w8a8_fp4_weight_t *w, int64_t K)
         return W8A8_ERR_INVALID_ARG;
     if ((w->codes == nullptr) != (w->scales == nullptr))
         return W8A8_ERR_INVALID_ARG;
-    if (w->codes == nullptr && w->w_bf16 == nullptr)
+    if (w->codes == nullptr && w->w_bf16 == nullptr && K > 0)
         return W8A8_ERR_INVALID_ARG;
     return W8A8_OK;
 }

@@ -1097,8 +1097,8 @@ w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
     const bool four = K > 0 && K % 32 == 0 && K <= kMaxTmaCoord && M <= kMaxTmaCoord && N <= kMaxTmaCoord &&
                       w->codes != nullptr && aligned16(x);
     if (!four) {
-        if (w->w_bf16 == nullptr)
-            return K > 0 && K % 32 == 0 && !aligned16(x) ? W8A8_ERR_ALIGNMENT : W8A8_ERR_SHAPE;
+        if (w->w_bf16 == nullptr && K > 0)
+            return K % 32 == 0 && !aligned16(x) ? W8A8_ERR_ALIGNMENT : W8A8_ERR_SHAPE;
         if (K > 0)
             W8A8_TRY(check_device_ptr(w->w_bf16));
         W8A8_TRY(bf16_impl(x, w->w_bf16, bias, y, M, K, N, st));

@@ -140,8 +140,15 @@ def _check(fn, code):
         raise err
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The device's current stream as a pointer.  The raw accessor makes no Stream object,
+    which costs 2 us of a small call's time."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _ptr(t):
@@ -500,12 +507,28 @@ def _fp4_tiles(rows, K, format):
     return (-(-rows // 128), -(-K // (4 * _FP4_BLOCK[format])), 512)
 
 
+def _fits(t, shape, dtype, device):
+    """Whether t is what _in accepts, in one expression: the small calls' common case."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous())
+
+
+def _column(t, shape, device, name):
+    """An optional BF16 input: checked, as its address (None where there is none)."""
+    if t is None:
+        return None
+    if not _fits(t, shape, torch.bfloat16, device):
+        _in(t, shape, torch.bfloat16, device, name)
+    return t.data_ptr()
+
+
 class FP4Tensor:
     """A matrix [rows, K] in 4-bit floating point: codes uint8 [rows, K/2] (two a byte, the
     even element in the low half), scales uint8 in the tiled layout of include/w8a8.h, and
-    for "nvfp4" the rows' float32 factors (None for "mxfp4")."""
+    for "nvfp4" the rows' float32 factors (None for "mxfp4").  One that the library fills
+    keeps all three in one buffer and makes these tensors, views of it, when asked."""
 
-    __slots__ = ("codes", "scales", "factor", "format", "rows", "K", "device")
+    __slots__ = ("rows", "K", "format", "device", "_ptrs", "_buffer", "_parts")
 
     def __init__(self, codes, scales, factor, format):
         fmt = _fp4_format(format)
@@ -513,22 +536,55 @@ class FP4Tensor:
         rows, half = codes.shape
         _fp4_k(2 * half)
         self.rows, self.K, self.format, self.device = rows, 2 * half, format, codes.device
-        _in(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device, "scales")
+        if not _fits(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device):
+            _in(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device, "scales")
         if fmt:
-            _in(factor, (rows,), torch.float32, codes.device, "factor")
+            if not _fits(factor, (rows,), torch.float32, codes.device):
+                _in(factor, (rows,), torch.float32, codes.device, "factor")
         elif factor is not None:
             raise ValueError("mxfp4 has no row factors")
-        self.codes, self.scales, self.factor = codes, scales, factor
+        self._buffer, self._parts = None, (codes, scales, factor)
+        self._ptrs = (codes.data_ptr(), scales.data_ptr(), factor.data_ptr() if fmt else None)
+
+    def _views(self):
+        if self._parts is None:
+            rows, half, buf = self.rows, self.K // 2, self._buffer
+            base = buf.data_ptr()
+            shape = _fp4_tiles(rows, self.K, self.format)
+            at = self._ptrs[1] - base
+            factor = None
+            if self._ptrs[2] is not None:
+                f = self._ptrs[2] - base
+                factor = buf[f:f + 4 * rows].view(torch.float32)
+            self._parts = (buf[:rows * half].view(rows, half), buf[at:at + math.prod(shape)].view(shape), factor)
+        return self._parts
+
+    @property
+    def codes(self):
+        return self._views()[0]
+
+    @property
+    def scales(self):
+        return self._views()[1]
+
+    @property
+    def factor(self):
+        return self._views()[2]
 
 
 def _fp4_empty(rows, K, format, device):
-    """A quantized matrix of this size, to be written."""
+    """A quantized matrix of this size, to be written: codes, scales (16-byte aligned) and
+    factors in one allocation."""
     _fp4_k(K)
     q = FP4Tensor.__new__(FP4Tensor)
-    q.rows, q.K, q.format, q.device = rows, K, format, device
-    q.codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=device)
-    q.scales = torch.empty(_fp4_tiles(rows, K, format), dtype=torch.uint8, device=device)
-    q.factor = torch.empty((rows,), dtype=torch.float32, device=device) if format == "nvfp4" else None
+    q.rows, q.K, q.format, q.device, q._parts = rows, K, format, device, None
+    rt, ct, _ = _fp4_tiles(rows, K, format)
+    at = (rows * K // 2 + 15) // 16 * 16
+    end = at + rt * ct * 512
+    nv = format == "nvfp4"
+    q._buffer = torch.empty(end + 4 * rows if nv else end, dtype=torch.uint8, device=device)
+    base = q._buffer.data_ptr()
+    q._ptrs = (base, base + at, base + end if nv else None)
     return q
 
 
@@ -567,10 +623,10 @@ def fp4_quantize(x, format="nvfp4", out=None):
     fmt = _fp4_format(format)
     _need(x, torch.bfloat16, "x")
     rows, K = x.shape
-    q = _fp4_out(out, rows, K, format, x.device)
-    _check("w8a8_fp4_quantize", lib().w8a8_fp4_quantize(
-        x.data_ptr(), rows, K, fmt, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor),
-        _stream(x.device)))
+    dev = x.device
+    q = _fp4_out(out, rows, K, format, dev)
+    _check("w8a8_fp4_quantize",
+           lib().w8a8_fp4_quantize(x.data_ptr(), rows, K, fmt, *q._ptrs, _stream(dev)))
     return q
 
 
@@ -580,8 +636,7 @@ def fp4_dequantize(q, out=None):
         raise TypeError("q must be an FP4Tensor")
     y = _out(out, (q.rows, q.K), torch.bfloat16, q.device, "out")
     _check("w8a8_fp4_dequantize", lib().w8a8_fp4_dequantize(
-        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), q.rows, q.K, FP4_FORMATS[q.format],
-        y.data_ptr(), _stream(q.device)))
+        *q._ptrs, q.rows, q.K, FP4_FORMATS[q.format], y.data_ptr(), _stream(q.device)))
     return y
 
 
@@ -607,10 +662,8 @@ class FP4Weight:
                     w_bf16 = None
         self.w, self.q, self.format = w_bf16, q, format
         self._rec = _FP4Weight(self.N, self.K, FP4_FORMATS[format],
-                               0 if w_bf16 is None else w_bf16.data_ptr(),
-                               0 if q is None else q.codes.data_ptr(),
-                               0 if q is None else q.scales.data_ptr(),
-                               0 if q is None or q.factor is None else q.factor.data_ptr())
+                               None if w_bf16 is None else w_bf16.data_ptr(),
+                               *((None, None, None) if q is None else q._ptrs))
 
     def record(self):
         return ctypes.byref(self._rec)
@@ -638,19 +691,20 @@ def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False
     M = math.prod(x.shape[:-1])
     dev = x.device
     _fp4_weight_on(weight, K, dev)
-    if bias is not None:
-        _in(bias, (weight.N,), torch.bfloat16, dev, "bias")
-    out = _out(out, (*x.shape[:-1], weight.N), torch.bfloat16, dev, "out")
+    b = _column(bias, (weight.N,), dev, "bias")
+    shape = (*x.shape[:-1], weight.N)
+    out = x.new_empty(shape) if out is None else _out(out, shape, torch.bfloat16, dev, "out")
     if workspace is None:
-        need = fp4_linear_workspace_bytes(M, K, weight.format)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        size = int(lib().w8a8_fp4_linear_workspace_bytes(M, K, FP4_FORMATS[weight.format]))
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
-        _out(workspace, (workspace.numel(),), torch.uint8, dev, "workspace")
-    path = ctypes.c_int(-1)
+        size = workspace.numel()
+        _out(workspace, (size,), torch.uint8, dev, "workspace")
+    path = ctypes.c_int(-1) if return_path else None
     _check("w8a8_fp4_linear", lib().w8a8_fp4_linear(
-        x.data_ptr(), M, K, weight.record(), _ptr(bias), out.data_ptr(), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), ctypes.byref(path), _stream(dev)))
+        x.data_ptr(), M, K, weight._rec, b, out.data_ptr(), workspace.data_ptr() if size else None, size,
+        path, _stream(dev)))
     return (out, path.value) if return_path else out
 
 
@@ -661,41 +715,35 @@ def fp4_linear_prequant(q, weight, bias=None, out=None):
     _fp4_weight_on(weight, q.K, q.device)
     if weight.format != q.format:
         raise ValueError(f"weight is {weight.format}, the activations {q.format}")
-    if bias is not None:
-        _in(bias, (weight.N,), torch.bfloat16, q.device, "bias")
+    b = _column(bias, (weight.N,), q.device, "bias")
     out = _out(out, (q.rows, weight.N), torch.bfloat16, q.device, "out")
     _check("w8a8_fp4_linear_prequant", lib().w8a8_fp4_linear_prequant(
-        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), q.rows, q.K, weight.record(),
-        _ptr(bias), out.data_ptr(), _stream(q.device)))
+        *q._ptrs, q.rows, q.K, weight._rec, b, out.data_ptr(), _stream(q.device)))
     return out
 
 
-def _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, h_out):
-    """Checks shared by both forms -> (M, K, T, device, h_out)."""
+def _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, res_scale, eps, h_out):
+    """Checks shared by both forms -> (h_out, the C call's arguments up to K)."""
     _need(h, torch.bfloat16, "h")
-    M, K = h.shape
+    shape = h.shape
+    M, K = shape
     dev = h.device
-    _in(y, (M, K), torch.bfloat16, dev, "y")
+    if not _fits(y, shape, torch.bfloat16, dev):
+        _in(y, shape, torch.bfloat16, dev, "y")
     if post_gamma is not None and not post_norm:
         raise ValueError("post_gamma needs post_norm")
-    if post_gamma is not None:
-        _in(post_gamma, (K,), torch.bfloat16, dev, "post_gamma")
-    if pre_gamma is not None:
-        _in(pre_gamma, (K,), torch.bfloat16, dev, "pre_gamma")
-    B = 1
-    for t in (gate, scale, shift):
-        if t is not None:
-            B = t.shape[0]
-            break
+    rows = gate if gate is not None else scale if scale is not None else shift
+    B = 1 if rows is None else rows.shape[0]
     if B == 0 or M % B:
         raise ValueError(f"gate, scale and shift must be [B, {K}] with B dividing M = {M}")
-    if gate is not None:
-        _in(gate, (B, K), torch.bfloat16, dev, "gate")
-    if scale is not None:
-        _in(scale, (B, K), torch.bfloat16, dev, "scale")
-    if shift is not None:
-        _in(shift, (B, K), torch.bfloat16, dev, "shift")
-    return M, K, max(M // B, 1), dev, _out(h_out, (M, K), torch.bfloat16, dev, "h_out")
+    if h_out is None:
+        h_out = torch.empty_like(h)
+    else:
+        _out(h_out, shape, torch.bfloat16, dev, "h_out")
+    return h_out, (h.data_ptr(), y.data_ptr(), int(post_norm), _column(post_gamma, (K,), dev, "post_gamma"),
+                   _column(gate, (B, K), dev, "gate"), res_scale, _column(pre_gamma, (K,), dev, "pre_gamma"),
+                   _column(scale, (B, K), dev, "scale"), _column(shift, (B, K), dev, "shift"), max(M // B, 1),
+                   eps, M, K)
 
 
 def block_norm(h, y, post_gamma=None, gate=None, pre_gamma=None, scale=None, shift=None, *,
@@ -705,13 +753,11 @@ def block_norm(h, y, post_gamma=None, gate=None, pre_gamma=None, scale=None, shi
     post_norm), n = bf16(RMSNorm(h') * pre_gamma * (1 + scale[b]) + shift[b]).  h, y [M, K],
     K a multiple of 8; gammas [K]; gate, scale, shift [B, K] with b = m // (M // B); each may
     be None.  h_out may be h (in place) -> (h', n)."""
-    M, K, T, dev, h_out = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm,
-                                           h_out)
-    n = _out(n_out, (M, K), torch.bfloat16, dev, "n_out")
-    _check("w8a8_block_norm", lib().w8a8_block_norm(
-        h.data_ptr(), y.data_ptr(), int(post_norm), _ptr(post_gamma), _ptr(gate), float(res_scale),
-        _ptr(pre_gamma), _ptr(scale), _ptr(shift), T, float(eps), M, K, h_out.data_ptr(),
-        n.data_ptr(), _stream(dev)))
+    h_out, args = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, res_scale, eps,
+                                   h_out)
+    n = torch.empty_like(h) if n_out is None else _out(n_out, h.shape, torch.bfloat16, h.device, "n_out")
+    _check("w8a8_block_norm",
+           lib().w8a8_block_norm(*args, h_out.data_ptr(), n.data_ptr(), _stream(h.device)))
     return h_out, n
 
 
@@ -720,13 +766,11 @@ def block_norm_fp4(h, y, format="nvfp4", post_gamma=None, gate=None, pre_gamma=N
     """block_norm with n quantized as fp4_quantize does, without being stored (the same bits
     as the two calls); K a multiple of 32 -> (h', FP4Tensor)."""
     fmt = _fp4_format(format)
-    M, K, T, dev, h_out = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm,
-                                           h_out)
-    q = _fp4_out(out, M, K, format, dev)
-    _check("w8a8_block_norm_fp4", lib().w8a8_block_norm_fp4(
-        h.data_ptr(), y.data_ptr(), int(post_norm), _ptr(post_gamma), _ptr(gate), float(res_scale),
-        _ptr(pre_gamma), _ptr(scale), _ptr(shift), T, float(eps), M, K, fmt, h_out.data_ptr(),
-        q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.factor), _stream(dev)))
+    h_out, args = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, res_scale, eps,
+                                   h_out)
+    q = _fp4_out(out, *h.shape, format, h.device)
+    _check("w8a8_block_norm_fp4",
+           lib().w8a8_block_norm_fp4(*args, fmt, h_out.data_ptr(), *q._ptrs, _stream(h.device)))
     return h_out, q
 
 

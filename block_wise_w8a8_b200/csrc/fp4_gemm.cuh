@@ -82,6 +82,17 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
 }
 
+// One lane of the converged warp.  The tcgen05 and TMA instructions below are issued under
+// this predicate, with the control flow and the operands around them the same in all lanes:
+// the compiler then keeps operands in uniform registers.  Issued by a thread picked with
+// lane == 0, each took about 60 cycles, 16 a slice against the 512 cycles of its products.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ pairs of CTAs
 // Tile 256 x 256, two CTAs of a cluster together (cta_group::2): each holds 128 rows of x and
 // 128 rows of w in shared memory and the accumulator of its 128 rows of y x all 256
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     PairSmem<kFmt> &sm = *reinterpret_cast<PairSmem<kFmt> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                              ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const uint32_t lane = lane_id();
     const uint32_t rank = norm::cluster_rank();
     volatile int *abort = &sm.abort;
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
+        {
             uint32_t it = 0;
             bool ok = true;
             for (int t = pair; ok && t < num_tiles; t += pairs) {
@@ -227,15 +238,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(&sm.full[s], 2 * kSliceBytes);
-                    const uint32_t bar = map_to(smem_u32(&sm.full[s]), 0);
-                    tma_load_pair(sm.a[s], &tmX, bar, ks * 128, row_x);
-                    tma_load_pair(sm.b[s], &tmW, bar, ks * 128, row_w);
-                    // scale maps count in 8-byte units: 64 a tile
-                    tma_load_pair(sm.sfa[s], &tmXs, bar, ks * (kTiles * 64), row_x >> 7);
-                    tma_load_pair(sm.sfb[s][0], &tmWs, bar, ks * (kTiles * 64), tn * 2);
-                    tma_load_pair(sm.sfb[s][1], &tmWs, bar, ks * (kTiles * 64), tn * 2 + 1);
+                    if (elect_one()) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&sm.full[s], 2 * kSliceBytes);
+                        const uint32_t bar = map_to(smem_u32(&sm.full[s]), 0);
+                        tma_load_pair(sm.a[s], &tmX, bar, ks * 128, row_x);
+                        tma_load_pair(sm.b[s], &tmW, bar, ks * 128, row_w);
+                        // scale maps count in 8-byte units: 64 a tile
+                        tma_load_pair(sm.sfa[s], &tmXs, bar, ks * (kTiles * 64), row_x >> 7);
+                        tma_load_pair(sm.sfb[s][0], &tmWs, bar, ks * (kTiles * 64), tn * 2);
+                        tma_load_pair(sm.sfb[s][1], &tmWs, bar, ks * (kTiles * 64), tn * 2 + 1);
+                    }
+                    __syncwarp();
                 }
             }
             if (!ok) {
@@ -248,7 +262,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t sfa = tmem + 512 - pair_sf_cols(kFmt);
             const uint32_t sfb = sfa + 4 * kTiles;
             uint32_t it = 0, i = 0;
@@ -265,30 +279,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t fa = smem_u32(sm.sfa[s]), fb0 = smem_u32(sm.sfb[s][0]), fb1 = smem_u32(sm.sfb[s][1]);
+                    if (elect_one()) {
+                        const uint32_t fa = smem_u32(sm.sfa[s]), fb0 = smem_u32(sm.sfb[s][0]), fb1 = smem_u32(sm.sfb[s][1]);
 #pragma unroll
-                    for (int j = 0; j < kTiles; ++j) {
-                        copy_scales<2>(sfa + 4 * j, fa + 512 * j);
-                        copy_scales<2>(sfb + 8 * j, fb0 + 512 * j);
-                        copy_scales<2>(sfb + 8 * j + 4, fb1 + 512 * j);
-                    }
-                    const uint64_t ad = umma_desc_sw128(smem_u32(sm.a[s]));
-                    const uint64_t bd = umma_desc_sw128(smem_u32(sm.b[s]));
+                        for (int j = 0; j < kTiles; ++j) {
+                            copy_scales<2>(sfa + 4 * j, fa + 512 * j);
+                            copy_scales<2>(sfb + 8 * j, fb0 + 512 * j);
+                            copy_scales<2>(sfb + 8 * j + 4, fb1 + 512 * j);
+                        }
+                        const uint64_t ad = umma_desc_sw128(smem_u32(sm.a[s]));
+                        const uint64_t bd = umma_desc_sw128(smem_u32(sm.b[s]));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int j = kFmt == kMx ? k >> 1 : k;
-                        const uint32_t id = idesc_fp4(256, 256, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
-                        umma_fp4<kFmt, 2>(d, ad + 2 * k, bd + 2 * k, id, sfa + 4 * j, sfb + 8 * j, (ks | k) != 0);
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = kFmt == kMx ? k >> 1 : k;
+                            const uint32_t id = idesc_fp4(256, 256, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
+                            umma_fp4<kFmt, 2>(d, ad + 2 * k, bd + 2 * k, id, sfa + 4 * j, sfb + 8 * j, (ks | k) != 0);
+                        }
+                        commit_pair(&sm.empty[s]);
+                        if (ks == p.slices - 1)
+                            commit_pair(&sm.tfull[i & 1]);
                     }
-                    commit_pair(&sm.empty[s]);
+                    __syncwarp();
                 }
-                if (ok)
-                    commit_pair(&sm.tfull[i & 1]);
             }
             // every product issued here completes before tensor memory is released
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             smem_u32(&sm.mma_done))
-                         : "memory");
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_u32(&sm.mma_done))
+                             : "memory");
+            __syncwarp();
             volatile int no_abort = 0;
             mbar_wait(&sm.mma_done, 0, &no_abort, 100000000ull);
         }
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     constexpr uint32_t kCols = BT + 8 * kTiles <= 64 ? 64 : (BT + 8 * kTiles <= 128 ? 128 : 256);
     extern __shared__ uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const uint32_t lane = lane_id();
     const int rank = static_cast<int>(norm::cluster_rank()), splits = static_cast<int>(norm::cluster_size());
     volatile int *abort = &sm.abort;
@@ -459,7 +478,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             uint32_t it = 0;
             bool ok = true;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
@@ -468,11 +487,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&sm.full[s], S::kStageBytes);
-                tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
-                tma_load_2d(sm.sfw[s], &tmWs, &sm.full[s], ks * (kTiles * 64), tn);
-                tma_load_2d(sm.x[s], &tmX, &sm.full[s], ks * 128, tm * BT);
-                tma_load_2d(sm.sfx[s], &tmXs, &sm.full[s], ks * (kTiles * 64), tm * BT / 128);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.full[s], S::kStageBytes);
+                    tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
+                    tma_load_2d(sm.sfw[s], &tmWs, &sm.full[s], ks * (kTiles * 64), tn);
+                    tma_load_2d(sm.x[s], &tmX, &sm.full[s], ks * 128, tm * BT);
+                    tma_load_2d(sm.sfx[s], &tmXs, &sm.full[s], ks * (kTiles * 64), tm * BT / 128);
+                }
+                __syncwarp();
             }
             if (!ok) {
                 volatile int no_abort = 0;
@@ -482,7 +504,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             const uint32_t sfw = tmem + BT, sfx = sfw + 4 * kTiles;
             uint32_t it = 0;
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
@@ -490,23 +512,27 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
                 if (!gemm::gemm_wait(&sm.full[s], ph, abort))
                     break;
                 tc_fence_after();
-                const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
+                if (elect_one()) {
+                    const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
-                    copy_scales<1>(sfw + 4 * j, fw + 512 * j);
-                    copy_scales<1>(sfx + 4 * j, fx + 512 * j);
-                }
-                const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
-                const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
+                    for (int j = 0; j < kTiles; ++j) {
+                        copy_scales<1>(sfw + 4 * j, fw + 512 * j);
+                        copy_scales<1>(sfx + 4 * j, fx + 512 * j);
+                    }
+                    const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
+                    const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = kFmt == kMx ? k >> 1 : k;
-                    const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
-                    umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = kFmt == kMx ? k >> 1 : k;
+                        const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
+                        umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
+                    }
+                    umma_commit(&sm.empty[s]);
+                    if (ks == ks1 - 1)
+                        umma_commit(&sm.tfull);
                 }
-                umma_commit(&sm.empty[s]);
+                __syncwarp();
             }
-            umma_commit(&sm.tfull);
         }
     }
     float *part = reinterpret_cast<float *>(sm.w);

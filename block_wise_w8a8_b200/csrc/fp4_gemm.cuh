@@ -138,9 +138,12 @@ __device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
+// Arrives on a barrier of either CTA.  Nothing written to memory is handed over (the tensor
+// memory loads before it have completed), so the release is left at its default scope, the
+// CTA: at cluster scope it waits for this thread's outstanding stores, over 1000 cycles.
 __device__ __forceinline__ void arrive_remote(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // TMA load into this CTA's shared memory that signals a barrier of the pair's even CTA.
 __device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1)

@@ -34,7 +34,6 @@ struct GemmParams {
     const float *wf;             // [N] row factors of w (kNv)
     const uint16_t *bias;        // [N] BF16 or null
     uint16_t *y;                 // [M, N] BF16
-    int32_t tma_y;               // y is stored by TMA (N a multiple of 8, y 16-byte aligned)
 };
 
 // Instruction descriptor of the block-scaled kinds, both operands E2M1 and K-major:
@@ -99,34 +98,51 @@ __device__ __forceinline__ bool elect_one()
 // columns in its tensor memory; the even CTA's MMA thread issues the products for both.
 // A slice then costs each SM 32 KB of codes and 4-6 KB of scales for 128 x 256 x 256
 // products.  One thread of each CTA loads its own half (signalling the even CTA's
-// barrier), four warps of each store their 128 rows.
+// barrier), the epilogue warps of each store their 128 rows.
+//
+// kTma: four epilogue warps, 64 columns at a time through shared memory to TMA stores.
+// Otherwise (N not a multiple of 8, or y not 16-byte aligned, where no TMA store can go) the
+// rows of y start at any even address and are stored two bytes a lane, which costs more
+// instructions; eight warps share them, two to the 32 rows of tensor memory that a warp may
+// read, 32 columns at a time (1000 x 2016 x 8191: 22 us, with four warps 30).  With TMA
+// eight warps are slower, 427 us for 407 at 16384 x 4096 x 16384.
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit in 512 columns,
 // so the accumulators share columns: one at 0, the other ending where the scales begin.
-// The epilogue reads the shared columns first and then lets the next tile's products
-// start, so only that first read is not overlapped.
+// The warps that read the shared columns read them first, and then the next tile's
+// products start, so only that first read is not overlapped.
 constexpr int kPairStages = 5;
-constexpr int kPairThreads = 192;
 constexpr int kPairGroup = 8;                // M tiles of a raster group
 
-template <int kFmt>
+template <bool kTma>
+struct PairEpi {
+    static constexpr int kWarps = kTma ? 4 : 8;
+    static constexpr int kParts = kWarps / 4;            // warps that share 32 rows
+    static constexpr int kWidth = 256 / kParts;          // columns of a warp
+    static constexpr int kChunk = kTma ? 64 : 32;        // columns a step
+    static constexpr int kThreads = 64 + 32 * kWarps;
+};
+
+template <int kFmt, bool kTma>
 struct alignas(1024) PairSmem {
+    using E = PairEpi<kTma>;
     uint8_t a[kPairStages][128 * 128];
     uint8_t b[kPairStages][128 * 128];
     uint8_t sfa[kPairStages][scale_slice_bytes(kFmt)];
     uint8_t sfb[kPairStages][2][scale_slice_bytes(kFmt)];
-    alignas(1024) uint8_t out[4][32 * 128];  // per epilogue warp: 32 rows x 64 BF16
-    float col[4][2][256];                    // per epilogue warp: row factors of w, bias
+    alignas(1024) uint8_t out[E::kWarps][32 * E::kChunk * 2];   // per epilogue warp: 32 rows
+    float col[E::kWarps][2][E::kWidth];      // per epilogue warp: row factors of w, bias
     uint64_t full[kPairStages];              // both CTAs' bytes (the even CTA's)
     uint64_t empty[kPairStages];
     uint64_t tfull[2];
-    uint64_t tdrained;                       // shared columns read (the even CTA's)
+    uint64_t tshared;                        // shared columns read (the even CTA's)
+    uint64_t tdrained[2];                    // accumulator read (the even CTA's)
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
 };
-template <int kFmt>
-constexpr size_t kPairSmemBytes = sizeof(PairSmem<kFmt>) + 1024;
+template <int kFmt, bool kTma>
+constexpr size_t kPairSmemBytes = sizeof(PairSmem<kFmt, kTma>) + 1024;
 
 // Tensor memory columns of the pair kernel: SFA and SFB of one slice at the end.
 __host__ __device__ constexpr uint32_t pair_sf_cols(int fmt) { return 12u * scale_tiles_a_slice(fmt); }
@@ -173,8 +189,8 @@ __device__ __forceinline__ void pair_tile(int t, const GemmParams &p, int &tm, i
     tn = local / gsz;
 }
 
-template <int kFmt>
-__global__ void __launch_bounds__(kPairThreads, 1)
+template <int kFmt, bool kTma>
+__global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmWs,
                      const __grid_constant__ CUtensorMap tmY, const GemmParams p)
@@ -183,8 +199,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr uint32_t kSfBytes = scale_slice_bytes(kFmt);
     constexpr uint32_t kSliceBytes = 2 * 128 * 128 + 3 * kSfBytes;
     extern __shared__ uint8_t smem_raw[];
-    PairSmem<kFmt> &sm = *reinterpret_cast<PairSmem<kFmt> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                             ~static_cast<uintptr_t>(1023));
+    using E = PairEpi<kTma>;
+    using S = PairSmem<kFmt, kTma>;
+    S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const uint32_t lane = lane_id();
     const uint32_t rank = norm::cluster_rank();
@@ -199,7 +216,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         mbar_init(&sm.tfull[0], 1);
         mbar_init(&sm.tfull[1], 1);
-        mbar_init(&sm.tdrained, 8);
+        mbar_init(&sm.tshared, 2 * 4);
+        mbar_init(&sm.tdrained[0], 2 * E::kWarps);
+        mbar_init(&sm.tdrained[1], 2 * E::kWarps);
         mbar_init(&sm.mma_done, 1);
         sm.abort = 0;
         fence_barrier_init();
@@ -207,7 +226,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmXs);
         prefetch_tensormap(&tmWs);
-        if (p.tma_y)
+        if (kTma)
             prefetch_tensormap(&tmY);
     }
     if (warp == 1) {
@@ -271,7 +290,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint32_t it = 0, i = 0;
             bool ok = true;
             for (int t = pair; ok && t < num_tiles; t += pairs, ++i) {
-                if (i > 0 && !gemm::gemm_wait(&sm.tdrained, (i - 1) & 1, abort))
+                // tile i - 2 has left this accumulator, tile i - 1 the columns both use
+                if (i > 1 && !gemm::gemm_wait(&sm.tdrained[i & 1], ((i >> 1) - 1) & 1, abort))
+                    break;
+                if (i > 0 && !gemm::gemm_wait(&sm.tshared, (i - 1) & 1, abort))
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem + (i & 1) * pair_acc1(kFmt);
@@ -318,8 +340,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // ---------------------------------------------------------------- epilogue
         const int ew = warp - 2;
         const int quarter = warp & 3;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t drained = map_to(smem_u32(&sm.tdrained), 0);
+        const int part = ew >> 2;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * E::kWidth;
+        const uint32_t shared = map_to(smem_u32(&sm.tshared), 0);
+        const uint32_t drained = map_to(smem_u32(&sm.tdrained[0]), 0);
         uint8_t *out = sm.out[ew];
         float *wf = sm.col[ew][0], *bias = sm.col[ew][1];
         uint32_t i = 0;
@@ -328,10 +352,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             pair_tile(t, p, tm, tn);
             const int64_t m_w = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32;
             const int64_t m = m_w + lane;
-            const int64_t n0 = static_cast<int64_t>(tn) * 256;
+            const int64_t n0 = static_cast<int64_t>(tn) * 256 + part * E::kWidth;
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < E::kWidth / 32; ++j) {
                 const int64_t n = n0 + j * 32 + lane;
                 wf[j * 32 + lane] = kFmt == kNv && n < p.N ? __ldg(p.wf + n) : 1.0f;
                 bias[j * 32 + lane] =
@@ -344,60 +368,80 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 break;
             tc_fence_after();
             const uint32_t acc = lane_base + buf * pair_acc1(kFmt);
+            // The columns that both accumulators use, the last 48 (kMx: 24) of the lower one and
+            // the first of the upper one, come first: in 64 columns, from one end or the other.
+            constexpr int kSteps = E::kWidth / E::kChunk;
+            constexpr int kSharedSteps = 64 / E::kChunk;
+            static_assert(pair_sf_cols(kFmt) <= 64, "shared columns");
+            const bool holds_shared = E::kParts == 1 || part != static_cast<int>(buf);
 #pragma unroll 1
-            for (int step = 0; step < 4; ++step) {
-                // the 64 columns that hold the shared ones come first
-                const int c = buf == 0 ? 3 - step : step;
-                uint32_t r[2][32];
-                tmem_ld32(acc + c * 64, r[0]);
-                tmem_ld32(acc + c * 64 + 32, r[1]);
-                tmem_wait_ld(r[0]);
-                tmem_wait_ld(r[1]);
-                if (step == 0) {
+            for (int step = 0; step < kSteps; ++step) {
+                const int c = buf == 0 ? kSteps - 1 - step : step;
+                uint32_t r[E::kChunk / 32][32];
+#pragma unroll
+                for (int q = 0; q < E::kChunk / 32; ++q)
+                    tmem_ld32(acc + c * E::kChunk + q * 32, r[q]);
+#pragma unroll
+                for (int q = 0; q < E::kChunk / 32; ++q)
+                    tmem_wait_ld(r[q]);
+                if (step == kSharedSteps - 1 && holds_shared) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        arrive_remote(drained);
+                        arrive_remote(shared);
                 }
-                if (lane == 0 && p.tma_y)
+                if (step == kSteps - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_remote(drained + buf * 8);
+                }
+                if (kTma && lane == 0)
                     gemm::tma_store_wait_read();
                 __syncwarp();
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
+                for (int g = 0; g < E::kChunk / 8; ++g) {
                     uint32_t o[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int e = g * 8 + q * 2;
-                        const float2 f = *reinterpret_cast<const float2 *>(wf + c * 64 + e);
-                        const float2 b = *reinterpret_cast<const float2 *>(bias + c * 64 + e);
+                        const float2 f = *reinterpret_cast<const float2 *>(wf + c * E::kChunk + e);
+                        const float2 b = *reinterpret_cast<const float2 *>(bias + c * E::kChunk + e);
                         const float v0 = __uint_as_float(r[e >> 5][e & 31]), v1 = __uint_as_float(r[e >> 5][(e & 31) + 1]);
                         o[q] = kFmt == kNv ? pack_bf16x2(fmaf(v0, xf * f.x, b.x), fmaf(v1, xf * f.y, b.y))
                                            : pack_bf16x2(v0 + b.x, v1 + b.y);
                     }
-                    st_shared_v4(out + lane * 128 + ((g ^ (lane & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                    st_shared_v4(out + (kTma ? lane * 128 + ((g ^ (lane & 7)) << 4) : gemm::stage_off(lane, g)),
+                                 make_uint4(o[0], o[1], o[2], o[3]));
                 }
-                const int64_t nc = n0 + c * 64;
-                if (p.tma_y) {
+                const int64_t nc = n0 + c * E::kChunk;
+                if (kTma) {
                     gemm::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && m_w < p.M && nc < p.N)
                         gemm::tma_store_2d(&tmY, out, static_cast<int32_t>(nc), static_cast<int32_t>(m_w));
                 } else {
                     __syncwarp();
-                    for (int rr = 0; rr < 32 && m_w + rr < p.M; ++rr) {
-                        uint16_t *dst = p.y + (m_w + rr) * p.N + nc;
+                    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - m_w));
+                    if (nc + lane < p.N) {
+                        uint16_t *dst = p.y + m_w * p.N + nc + lane;
+                        const uint8_t *src = out + (lane & 7) * 2;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int e = h * 32 + static_cast<int>(lane);
-                            if (nc + e < p.N)
-                                dst[e] = *reinterpret_cast<const uint16_t *>(out + rr * 128 + (((e >> 3) ^ (rr & 7)) << 4) +
-                                                                             (e & 7) * 2);
+                        for (int r0 = 0; r0 < 32; r0 += 16) {
+                            uint16_t v[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] = *reinterpret_cast<const uint16_t *>(src + gemm::stage_off(r0 + j, lane >> 3));
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (r0 + j < rows)
+                                    dst[(r0 + j) * p.N] = v[j];
                         }
                     }
                 }
             }
         }
-        if (lane == 0 && p.tma_y)
+        if (kTma && lane == 0)
             gemm::tma_store_wait_all();
     }
     tc_fence_before();
@@ -414,14 +458,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // y^T: the weight's rows are the 128 rows of a product and BT tokens its columns, so that a
 // tile costs the weight's bytes and little else.  One tile a CTA; the K slices are split
 // over the S CTAs of a cluster, which add their FP32 partial tiles through distributed
-// shared memory in rank order (the result does not depend on timing).
+// shared memory in rank order (the result does not depend on timing).  The pipeline takes
+// less than half of an SM's shared memory: two CTAs a SM keep all SMs streaming when the
+// tiles do not divide among them.
+//
+// kQuant: x is BF16 and quantized on the way in.  Each CTA codes the slices that it
+// multiplies, four warps writing them into the pipeline's stages in the layout that the TMA
+// would; the weight's loads run ahead meanwhile.  For a few rows this repeated work costs
+// less than a launch of the quantizer and its workspace.
 constexpr int kSkinnyThreads = 192;
 
 template <int kFmt, int BT>
 struct alignas(1024) SkinnySmem {
     static constexpr int kStageBytes = 128 * 128 + BT * 128 + 2 * scale_slice_bytes(kFmt);
-    static constexpr int kStages = 204800 / kStageBytes < 8 ? 204800 / kStageBytes : 8;
-    uint8_t w[kStages][128 * 128];       // after the last product: partial [BT][128] FP32
+    static constexpr int kStages = BT < 64 ? 4 : 3;
+    uint8_t w[kStages][128 * 128];       // after the last product, with x: partial [BT][128] FP32
     uint8_t x[kStages][BT * 128];
     uint8_t sfw[kStages][scale_slice_bytes(kFmt)];
     uint8_t sfx[kStages][scale_slice_bytes(kFmt)];
@@ -430,20 +481,110 @@ struct alignas(1024) SkinnySmem {
     uint64_t tfull;
     uint32_t tmem_base;
     int abort;
-    static_assert(BT * 128 * 4 <= kStages * 128 * 128, "partial tile does not fit");
+    uint32_t top[4][4];                  // kQuant: per warp and row, the largest magnitude
+    float factor[4];                     // kQuant: row factors
+    static_assert(BT * 128 * 4 <= kStages * (128 * 128 + BT * 128), "partial tile does not fit");
 };
 template <int kFmt, int BT>
 constexpr size_t kSkinnySmemBytes = sizeof(SkinnySmem<kFmt, BT>) + 1024;
+constexpr int kQuantRows = 4;            // most rows of kQuant
 
-template <int kFmt, int BT>
-__global__ void __launch_bounds__(kSkinnyThreads, 1)
+// kQuant, kNv: the row factors, from the rows' largest magnitudes over all of K.  Runs before
+// the CTA's set-up is complete, so that its loads overlap it; four warps.
+template <class S>
+__device__ __forceinline__ void row_tops(S &sm, const GemmParams &p, const uint16_t *x, int tid, uint32_t lane)
+{
+    // 4 pieces of 8 values of every row in flight
+    uint32_t top[kQuantRows] = {};
+    const int64_t pieces = p.K / 8;
+    for (int64_t c0 = tid; c0 < pieces; c0 += 4 * 128) {
+        uint4 v[kQuantRows][4];
+#pragma unroll
+        for (int m = 0; m < kQuantRows; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[m][i] = m < p.M && c0 + i * 128 < pieces
+                              ? __ldg(reinterpret_cast<const uint4 *>(x + m * p.K) + c0 + i * 128)
+                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < kQuantRows; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                top[m] = __vmaxu2(top[m], __vmaxu2(__vmaxu2(v[m][i].x & 0x7FFF7FFFu, v[m][i].y & 0x7FFF7FFFu),
+                                                   __vmaxu2(v[m][i].z & 0x7FFF7FFFu, v[m][i].w & 0x7FFF7FFFu)));
+    }
+#pragma unroll
+    for (int m = 0; m < kQuantRows; ++m) {
+        const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, max(top[m] & 0xFFFFu, top[m] >> 16));
+        if (lane == 0)
+            sm.top[tid >> 5][m] = t;
+    }
+}
+
+// kQuant's four warps: the CTA's slices of x, coded into the stages.  Thread i takes block
+// i % 16 of 16 values of a slice, row i / 16.
+template <int kFmt, class S>
+__device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, const uint16_t *x, int ks0, int ks1, int tid,
+                                                uint32_t lane, volatile int *abort)
+{
+    const int64_t nb = p.K / 16;
+    const int b = tid & 15, r = tid >> 4;
+    const bool mine = r < p.M;
+    const uint16_t *src = x + r * p.K;
+    uint32_t w[8] = {};
+    if (mine && static_cast<int64_t>(ks0) * 16 + b < nb)
+        load16(src + (static_cast<int64_t>(ks0) * 16 + b) * 16, w);
+    Row row{};
+    if (kFmt == kNv) {
+        uint32_t t = 0;
+        for (int i = 0; i < 4; ++i)
+            t = max(t, sm.top[i][r & (kQuantRows - 1)]);
+        row = row_of(t);
+        if (b == 0 && r < kQuantRows)
+            sm.factor[r] = row.factor;
+    }
+    uint32_t it = 0;
+    for (int ks = ks0; ks < ks1; ++ks, ++it) {
+        const uint32_t s = it % S::kStages, ph = (it / S::kStages) & 1;
+        const bool in = mine && static_cast<int64_t>(ks) * 16 + b < nb;
+        uint32_t m = in ? amax16(w) : 0, byte = 0;
+        if (kFmt == kMx)
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        uint2 o = make_uint2(0, 0);
+        if (in)
+            o = encode16<kFmt>(w, m, row, byte);
+        const uint32_t word = gather_scales<kFmt>(byte);
+        const int64_t nx = static_cast<int64_t>(ks + 1) * 16 + b;
+        if (mine && ks + 1 < ks1 && nx < nb)
+            load16(src + nx * 16, w);
+        if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort))
+            break;
+        if (mine) {
+            *reinterpret_cast<uint2 *>(sm.x[s] + r * 128 + (((b >> 1) ^ (r & 7)) << 4) + (b & 1) * 8) = o;
+            if (stores_scales<kFmt>(b))
+                *reinterpret_cast<uint32_t *>(sm.sfx[s] + (b / (kFmt == kNv ? 4 : 8)) * 512 + r * 16) = word;
+        }
+        gemm::fence_proxy_async_smem();      // the products read shared memory as the TMA does
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.full[s]);
+    }
+    // every thread of the epilogue reads the factors
+    if (kFmt == kNv)
+        named_bar_sync(1, 128);
+}
+
+template <int kFmt, int BT, bool kQuant>
+__global__ void __launch_bounds__(kSkinnyThreads, 2)
     gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmWs,
-                       const GemmParams p)
+                       const uint16_t *x, const GemmParams p)
 {
     using S = SkinnySmem<kFmt, BT>;
     constexpr int kTiles = scale_tiles_a_slice(kFmt);
     constexpr int kStages = S::kStages;
+    constexpr uint32_t kTxBytes =
+        kQuant ? 128 * 128 + scale_slice_bytes(kFmt) : static_cast<uint32_t>(S::kStageBytes);
     constexpr uint32_t kCols = BT + 8 * kTiles <= 64 ? 64 : (BT + 8 * kTiles <= 128 ? 128 : 256);
     extern __shared__ uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -459,21 +600,25 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[s], kQuant ? 5 : 1);
             mbar_init(&sm.empty[s], 1);
         }
         mbar_init(&sm.tfull, 1);
         sm.abort = 0;
         fence_barrier_init();
-        prefetch_tensormap(&tmX);
         prefetch_tensormap(&tmW);
-        prefetch_tensormap(&tmXs);
         prefetch_tensormap(&tmWs);
+        if (!kQuant) {
+            prefetch_tensormap(&tmX);
+            prefetch_tensormap(&tmXs);
+        }
     }
     if (warp == 1) {
         tmem_alloc(&sm.tmem_base, kCols);
         tmem_relinquish();
     }
+    if (kQuant && kFmt == kNv && warp >= 2)
+        row_tops(sm, p, x, static_cast<int>(threadIdx.x) - 64, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -481,109 +626,143 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.full[s], S::kStageBytes);
-                    tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
-                    tma_load_2d(sm.sfw[s], &tmWs, &sm.full[s], ks * (kTiles * 64), tn);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int ks = ks0; ks < ks1; ++ks, ++it) {
+            const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+            if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort)) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.full[s], kTxBytes);
+                tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
+                tma_load_2d(sm.sfw[s], &tmWs, &sm.full[s], ks * (kTiles * 64), tn);
+                if (!kQuant) {
                     tma_load_2d(sm.x[s], &tmX, &sm.full[s], ks * 128, tm * BT);
                     tma_load_2d(sm.sfx[s], &tmXs, &sm.full[s], ks * (kTiles * 64), tm * BT / 128);
                 }
-                __syncwarp();
             }
-            if (!ok) {
-                volatile int no_abort = 0;
-                const uint32_t first = it > kStages ? it - kStages : 0;
-                for (uint32_t j = first; j < it; ++j)
-                    mbar_wait(&sm.full[j % kStages], (j / kStages) & 1, &no_abort, 100000000ull);
-            }
+            __syncwarp();
+        }
+        if (!ok) {
+            // copies in flight land before shared memory is released: they need
+            // microseconds, this waits a millisecond for them
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull)
+                ;
         }
     } else if (warp == 1) {
-        {
-            const uint32_t sfw = tmem + BT, sfx = sfw + 4 * kTiles;
-            uint32_t it = 0;
-            for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                if (!gemm::gemm_wait(&sm.full[s], ph, abort))
-                    break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
+        const uint32_t sfw = tmem + BT, sfx = sfw + 4 * kTiles;
+        uint32_t it = 0;
+        for (int ks = ks0; ks < ks1; ++ks, ++it) {
+            const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+            if (!gemm::gemm_wait(&sm.full[s], ph, abort))
+                break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
 #pragma unroll
-                    for (int j = 0; j < kTiles; ++j) {
-                        copy_scales<1>(sfw + 4 * j, fw + 512 * j);
-                        copy_scales<1>(sfx + 4 * j, fx + 512 * j);
-                    }
-                    const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
-                    const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int j = kFmt == kMx ? k >> 1 : k;
-                        const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
-                        umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
-                    }
-                    umma_commit(&sm.empty[s]);
-                    if (ks == ks1 - 1)
-                        umma_commit(&sm.tfull);
+                for (int j = 0; j < kTiles; ++j) {
+                    copy_scales<1>(sfw + 4 * j, fw + 512 * j);
+                    copy_scales<1>(sfx + 4 * j, fx + 512 * j);
                 }
-                __syncwarp();
+                const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
+                const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = kFmt == kMx ? k >> 1 : k;
+                    const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
+                    umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
+                }
+                umma_commit(&sm.empty[s]);
+                if (ks == ks1 - 1)
+                    umma_commit(&sm.tfull);
             }
+            __syncwarp();
         }
+    } else if (kQuant) {
+        quantize_slices<kFmt>(sm, p, x, ks0, ks1, static_cast<int>(threadIdx.x) - 64, lane, abort);
     }
+    // The epilogue's thread owns output n and the tokens of this CTA's tile.
     float *part = reinterpret_cast<float *>(sm.w);
-    if (warp >= 2) {
-        const int quarter = warp & 3;
-        const int row = quarter * 32 + static_cast<int>(lane);
-        const int64_t n = static_cast<int64_t>(tn) * 128 + row;
-        const bool ok = gemm::gemm_wait(&sm.tfull, 0, abort);
+    const int row = (warp & 3) * 32 + static_cast<int>(lane);
+    const int64_t n = static_cast<int64_t>(tn) * 128 + row;
+    const int64_t m0 = static_cast<int64_t>(tm) * BT;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(BT), p.M - m0));
+    const bool store = warp >= 2 && n < p.N;
+    float wf = 1.0f, bias = 0.0f;
+    if (store) {
+        if (kFmt == kNv)
+            wf = __ldg(p.wf + n);
+        if (p.bias != nullptr)
+            bias = __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16);
+    }
+    auto finish = [&](float v, int t) {
+        const int64_t m = m0 + t;
+        if (kFmt == kNv)
+            v = fmaf(v, (kQuant ? sm.factor[t] : __ldg(p.xf + m)) * wf, bias);
+        else
+            v = v + bias;
+        p.y[m * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    };
+    if (warp >= 2 && gemm::gemm_wait(&sm.tfull, 0, abort)) {
         tc_fence_after();
-        const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        if (ok) {
+        const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < tokens; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(acc + c, v);
+            tmem_wait_ld(v);
 #pragma unroll
-            for (int c = 0; c < BT; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(acc + c, r);
-                tmem_wait_ld(r);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    part[(c + i) * 128 + row] = __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) {
+                if (splits > 1)
+                    part[(c + i) * 128 + row] = __uint_as_float(v[i]);
+                else if (store && c + i < tokens)
+                    finish(__uint_as_float(v[i]), c + i);
             }
         }
-        (void)n;
     }
     tc_fence_before();
     __syncthreads();
-    norm::cluster_barrier();     // every rank's partial tile is in its shared memory
-    if (warp >= 2 && !*abort) {
-        const int row = static_cast<int>(threadIdx.x) - 64;
-        const int64_t n = static_cast<int64_t>(tn) * 128 + row;
-        if (n < p.N) {
-            const float wf = kFmt == kNv ? __ldg(p.wf + n) : 1.0f;
-            const float b = p.bias != nullptr ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16) : 0.0f;
-            for (int t = rank; t < BT && static_cast<int64_t>(tm) * BT + t < p.M; t += splits) {
-                const int64_t m = static_cast<int64_t>(tm) * BT + t;
-                float v = 0.0f;
-                for (int q = 0; q < splits; ++q) {
-                    float u;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(u)
-                                 : "r"(map_to(smem_u32(part + t * 128 + row), static_cast<uint32_t>(q))));
-                    v += u;
+    if (splits > 1) {
+        norm::cluster_barrier();     // every rank's partial tile is in its shared memory
+        // tokens are dealt out to the ranks in equal runs
+        const int each = (tokens + splits - 1) / splits;
+        const int t1 = min(tokens, (rank + 1) * each);
+        if (store && !*abort) {
+            // 8 tokens of 4 ranks in flight: a read of another SM's shared memory takes about
+            // as long as one of L2
+            for (int t0 = rank * each; t0 < t1; t0 += 8) {
+                float v[8] = {};
+                for (int q0 = 0; q0 < splits; q0 += 4) {
+                    float u[4][8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (q0 + q >= splits)
+                            break;
+                        const uint32_t base = map_to(smem_u32(part + t0 * 128 + row), static_cast<uint32_t>(q0 + q));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[q][i]) : "r"(base + i * 512));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (q0 + q >= splits)
+                            break;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] += u[q][i];
+                    }
                 }
-                v = kFmt == kNv ? fmaf(v, __ldg(p.xf + m) * wf, b) : v + b;
-                p.y[m * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (t0 + i < t1)
+                        finish(v[i], t0 + i);
             }
         }
+        norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
     }
-    norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
     if (warp == 1)
         tmem_dealloc(tmem, kCols);
 }

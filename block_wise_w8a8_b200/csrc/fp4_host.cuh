@@ -93,7 +93,7 @@ struct Fp4Operand {
     const float *factor;
 };
 
-template <int kFmt>
+template <int kFmt, bool kTma>
 w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream, bool pdl)
 {
     int dev;
@@ -101,16 +101,15 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
     CUtensorMap mx, mxs, mw, mws, my;
     W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, 128, mx, mxs));
     W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 128, mw, mws));
-    p.tma_y = p.N % 8 == 0 && aligned16(p.y);
     my = mx;
-    if (p.tma_y)
+    if (kTma)
         W8A8_TRY(make_map(my, p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.M, p.N, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
     p.num_tm = static_cast<int32_t>((p.M + 255) / 256);
     p.num_tn = static_cast<int32_t>((p.N + 255) / 256);
     if (static_cast<int64_t>(p.num_tm) * p.num_tn >= (int64_t{1} << 30))
         return W8A8_ERR_SHAPE;
-    auto kern = fp4::gemm_pair_kernel<kFmt>;
-    constexpr size_t smem = fp4::kPairSmemBytes<kFmt>;
+    auto kern = fp4::gemm_pair_kernel<kFmt, kTma>;
+    constexpr size_t smem = fp4::kPairSmemBytes<kFmt, kTma>;
     static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -120,7 +119,7 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(fp4::kPairThreads);
+    cfg.blockDim = dim3(fp4::PairEpi<kTma>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -128,7 +127,7 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
     int pairs;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        int &known = g_dev[dev].fp4_pairs[kFmt];
+        int &known = g_dev[dev].fp4_pairs[kFmt * 2 + kTma];
         if (known == 0) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        static_cast<int>(smem));
@@ -150,23 +149,28 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
     return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
-template <int kFmt, int BT>
-w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream, bool pdl)
+// xb: BF16 activations to quantize on the way (kQuant), else null.
+template <int kFmt, int BT, bool kQuant>
+w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const Fp4Operand &w, fp4::GemmParams p,
+                                cudaStream_t stream, bool pdl)
 {
     int dev;
     W8A8_TRY(current_device(dev));
     CUtensorMap mx, mxs, mw, mws;
-    W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, BT, mx, mxs));
     W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 128, mw, mws));
+    mx = mw;
+    mxs = mws;
+    if (!kQuant)
+        W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, BT, mx, mxs));
     p.num_tm = static_cast<int32_t>((p.M + BT - 1) / BT);
     p.num_tn = static_cast<int32_t>((p.N + 127) / 128);
     const int64_t tiles = static_cast<int64_t>(p.num_tm) * p.num_tn;
     if (tiles >= (int64_t{1} << 27))
         return W8A8_ERR_SHAPE;
-    auto kern = fp4::gemm_skinny_kernel<kFmt, BT>;
+    auto kern = fp4::gemm_skinny_kernel<kFmt, BT, kQuant>;
     constexpr size_t smem = fp4::kSkinnySmemBytes<kFmt, BT>;
     static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
-    constexpr int slot = kFmt * 4 + (BT == 16 ? 0 : BT == 32 ? 1 : BT == 64 ? 2 : 3);
+    constexpr int slot = kFmt * 5 + (kQuant ? 4 : BT == 16 ? 0 : BT == 32 ? 1 : BT == 64 ? 2 : 3);
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!g_dev[dev].fp4_skinny_attr_set[slot]) {
@@ -177,8 +181,11 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const Fp4Operand &w, fp4::G
             g_dev[dev].fp4_skinny_attr_set[slot] = true;
         }
     }
+    // K is split while that makes no more CTAs than fit on the device (two a SM) and leaves
+    // each enough slices: 4 in clusters of up to 4 (1 x 4096 x 4096: 7.7 us unsplit, 6.7, 6.0
+    // in clusters of 2, 4 and 7.4 of 8), 8 in clusters of 8 (1 x 16384 x 4096: 12.1, 11.6 us).
     int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= g_dev[dev].sms && splits * 2 <= p.slices)
+    while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].sms && p.slices >= splits * 2 * (splits < 4 ? 4 : 8))
         splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -194,7 +201,7 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const Fp4Operand &w, fp4::G
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, xb, p);
     return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
@@ -203,18 +210,23 @@ w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const 
                                 bool pdl)
 {
     if (p.M <= 16)
-        return launch_fp4_skinny<kFmt, 16>(x, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 16, false>(x, nullptr, w, p, stream, pdl);
     if (p.M <= 32)
-        return launch_fp4_skinny<kFmt, 32>(x, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 32, false>(x, nullptr, w, p, stream, pdl);
     if (p.M <= 64)
-        return launch_fp4_skinny<kFmt, 64>(x, w, p, stream, pdl);
-    if (p.M <= 128)
-        return launch_fp4_skinny<kFmt, 128>(x, w, p, stream, pdl);
-    return launch_fp4_pair<kFmt>(x, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 64, false>(x, nullptr, w, p, stream, pdl);
+    // From 65 tokens on the pair kernel is the faster one where its tiles fill enough of the
+    // device: 128 x 4096 x 16384 15.2 us for 18.3, 128 x 2048 x 8192 10.5 for 13.3; but
+    // 128 x 4096 x 4096, 16 tiles that it does not split along K, 12.3 for 11.5 and
+    // 128 x 16384 x 4096 27.4 for 18.9.
+    if (p.M <= 128 && p.N <= 4096)
+        return launch_fp4_skinny<kFmt, 128, false>(x, nullptr, w, p, stream, pdl);
+    return p.N % 8 == 0 && aligned16(p.y) ? launch_fp4_pair<kFmt, true>(x, w, p, stream, pdl)
+                                          : launch_fp4_pair<kFmt, false>(x, w, p, stream, pdl);
 }
 
-w8a8_status_t launch_fp4_gemm(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
-                              const uint16_t *bias, uint16_t *y, cudaStream_t stream, bool pdl)
+fp4::GemmParams fp4_gemm_params(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
+                                const uint16_t *bias, uint16_t *y)
 {
     fp4::GemmParams p{};
     p.M = M;
@@ -225,9 +237,27 @@ w8a8_status_t launch_fp4_gemm(const Fp4Operand &x, int64_t M, int64_t K, const w
     p.wf = w->factor;
     p.bias = bias;
     p.y = y;
+    return p;
+}
+
+w8a8_status_t launch_fp4_gemm(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
+                              const uint16_t *bias, uint16_t *y, cudaStream_t stream, bool pdl)
+{
+    const fp4::GemmParams p = fp4_gemm_params(x, M, K, w, bias, y);
     const Fp4Operand wo{w->codes, w->scales, w->factor};
     return w->format == W8A8_FP4_MX ? launch_fp4_gemm_t<fp4::kMx>(x, wo, p, stream, pdl)
                                     : launch_fp4_gemm_t<fp4::kNv>(x, wo, p, stream, pdl);
+}
+
+// The linear of at most fp4::kQuantRows rows: quantization and product in one kernel.
+w8a8_status_t launch_fp4_linear_few(const uint16_t *x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
+                                    const uint16_t *bias, uint16_t *y, cudaStream_t stream)
+{
+    const fp4::GemmParams p = fp4_gemm_params(Fp4Operand{}, M, K, w, bias, y);
+    const Fp4Operand wo{w->codes, w->scales, w->factor};
+    return w->format == W8A8_FP4_MX
+               ? launch_fp4_skinny<fp4::kMx, 16, true>(Fp4Operand{}, x, wo, p, stream, false)
+               : launch_fp4_skinny<fp4::kNv, 16, true>(Fp4Operand{}, x, wo, p, stream, false);
 }
 
 // A weight record: consistent fields; the buffers are checked by whoever uses them.

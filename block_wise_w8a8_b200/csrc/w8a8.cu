@@ -35,8 +35,8 @@ struct DeviceInfo {
     bool rstd_attr_set = false;
     bool norm_attr_set[4] = {false, false, false, false};
     int norm_max_clusters[norm::kMaxCluster + 1] = {};    // by cluster size, 0 = unknown
-    int fp4_pairs[2] = {0, 0};                             // by format: pairs that fit, 0 = unknown
-    bool fp4_skinny_attr_set[8] = {};                      // by format and token tile
+    int fp4_pairs[4] = {};                                 // by format and store: pairs that fit, 0 = unknown
+    bool fp4_skinny_attr_set[10] = {};                     // by format and token tile, quantizing or not
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -1069,7 +1069,7 @@ w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, c
 
 size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format)
 {
-    if (M <= 0 || K <= 0 || K % 32 || !fp4_format_ok(format))
+    if (M <= fp4::kQuantRows || K <= 0 || K % 32 || !fp4_format_ok(format))
         return 0;
     return round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2)) + fp4_scale_bytes(M, K, format) +
            (format == W8A8_FP4_NV ? static_cast<size_t>(M) * sizeof(float) : 0);
@@ -1107,6 +1107,12 @@ w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
         return W8A8_OK;
     }
     W8A8_TRY(check_fp4(w->codes, w->scales, w->factor, w->format));
+    if (M <= fp4::kQuantRows) {
+        W8A8_TRY(launch_fp4_linear_few(x, M, K, w, bias, y, st));
+        if (path_taken != nullptr)
+            *path_taken = W8A8_PATH_FP4;
+        return W8A8_OK;
+    }
     if (workspace == nullptr || !aligned16(workspace) ||
         workspace_bytes < w8a8_fp4_linear_workspace_bytes(M, K, w->format))
         return W8A8_ERR_WORKSPACE;

@@ -361,7 +361,8 @@ W8A8_API w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *
                                            w8a8_bf16_t *y, void *stream);
 
 /* Bytes of device workspace of w8a8_fp4_linear: the quantized activations.  0 when K is not
- * a positive multiple of 32 (the BF16 path) or M is 0. */
+ * a positive multiple of 32 (the BF16 path) or M is at most 4 (they are then quantized
+ * inside the product). */
 W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format);
 
 /* Y[M, N] = X[M, K] W^T + bias with X quantized in the call to the weight's format:

@@ -12,18 +12,25 @@
 // output is that of the quantizer of fp4.cuh on n, code for code.
 //
 // Bound by HBM: h and y are read, h' and n written once (8 bytes a value, 6.6 with 4-bit
-// output).  W warps share a row and keep its h and y, later h' and n, in registers; the
-// sums of squares go through shuffles and shared memory.  The column factors are read
-// through L1, which a row's neighbours keep warm.
+// output).  W warps share a row and keep its h and y, then h' and n, in registers, P pieces
+// of 8 values a lane; the sums of squares go through shuffles and shared memory.
+//
+//   stream_kernel  many rows: CTAs stay, take every gridDim.x-th row, and have the next rows'
+//                  h and y copied into a ring in shared memory (one bulk copy each) while they
+//                  work.  A lane has the same columns in every row: for P <= 2 their factors
+//                  stay in registers and are read again when the rows' group b changes; for
+//                  P = 4 they come from L1 or L2 where they are used.
+//   row_kernel     few rows, or rows too long for the ring: one row a W warps, straight from
+//                  global memory; longer rows are read again for each pass (kLong).
 #pragma once
 
 #include "common.cuh"
 #include "fp4.cuh"
+#include "norm.cuh"
 
 namespace w8a8 {
 namespace bnorm {
 
-constexpr int kWarps = 8;                        // warps of a CTA
 constexpr int kOutBf16 = -1;                     // else fp4::kMx / fp4::kNv
 
 struct Params {
@@ -33,51 +40,73 @@ struct Params {
     int64_t M, M_pad, K, T;                      // M_pad: M rounded up to 128 for 4-bit output
     float eps, res_scale;
     int32_t post_norm;
+    int32_t stages;                              // stream_kernel: rows in the ring
     uint16_t *h_out;                             // [M, K], may be h
     uint16_t *n_out;                             // [M, K] (BF16 output)
     uint8_t *codes, *scales;                     // 4-bit output, as the quantizer's
     float *factor;
 };
 
-template <int V>
-__device__ __forceinline__ void load_row(const uint16_t *p, uint32_t (&w)[V / 2])
+__device__ __forceinline__ void unpack4(const uint4 a, uint32_t (&w)[4])
 {
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+}
+__device__ __forceinline__ uint4 pack4(const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+// The factors of 8 columns in FP32: u = (y rstd) post, n = (h' rstd) pre + shift, with
+// post = fl(post_gamma gate) and pre = fl(pre_gamma fl(1 + scale)); 1 and 0 where they are
+// left out.
+struct Post {
+    float2 post[4];
+};
+struct Pre {
+    float2 pre[4], shift[4];
+};
+__device__ __forceinline__ void load_factor(const uint16_t *p, float none, float2 (&f)[4])
+{
+    if (p != nullptr) {
+        uint32_t w[4];
+        unpack4(__ldg(reinterpret_cast<const uint4 *>(p)), w);
 #pragma unroll
-    for (int i = 0; i < V / 8; ++i) {
-        const uint4 a = *(reinterpret_cast<const uint4 *>(p) + i);
-        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+        for (int i = 0; i < 4; ++i)
+            f[i] = pair_of(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(none, none);
     }
 }
-template <int V>
-__device__ __forceinline__ void load_col(const uint16_t *p, uint32_t (&w)[V / 2])
+__device__ __forceinline__ void load_post(const Params &p, int64_t col, int64_t mod, Post &c)
 {
+    float2 gate[4];
+    load_factor(p.post_gamma == nullptr ? nullptr : p.post_gamma + col, 1.0f, c.post);
+    load_factor(p.gate == nullptr ? nullptr : p.gate + mod + col, 1.0f, gate);
 #pragma unroll
-    for (int i = 0; i < V / 8; ++i) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
-    }
+    for (int i = 0; i < 4; ++i)
+        c.post[i] = __fmul2_rn(c.post[i], gate[i]);
 }
-template <int V>
-__device__ __forceinline__ void store_row(uint16_t *p, const uint32_t (&w)[V / 2])
+__device__ __forceinline__ void load_pre(const Params &p, int64_t col, int64_t mod, Pre &c)
 {
+    float2 scale[4];
+    load_factor(p.pre_gamma == nullptr ? nullptr : p.pre_gamma + col, 1.0f, c.pre);
+    load_factor(p.scale == nullptr ? nullptr : p.scale + mod + col, 0.0f, scale);
+    load_factor(p.shift == nullptr ? nullptr : p.shift + mod + col, 0.0f, c.shift);
 #pragma unroll
-    for (int i = 0; i < V / 8; ++i)
-        *(reinterpret_cast<uint4 *>(p) + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < 4; ++i)
+        c.pre[i] = __fmul2_rn(c.pre[i], __fadd2_rn(make_float2(1.0f, 1.0f), scale[i]));
 }
 
-template <int V>
-__device__ __forceinline__ float squares(const uint32_t (&w)[V / 2])
+__device__ __forceinline__ void add_squares(const uint32_t (&w)[4], float2 &acc)
 {
-    float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        a = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), a);
-        b = fmaf(bf16_hi(w[i]), bf16_hi(w[i]), b);
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = pair_of(w[i]);
+        acc = __ffma2_rn(v, v, acc);
     }
-    return a + b;
 }
 
-// Sum (or maximum) over the W warps of a row; every thread of the CTA takes part.
+// Sum (or maximum) over the W warps of a row through s[W]; every thread of the row takes part.
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float *s, int warp, uint32_t lane)
 {
@@ -91,202 +120,304 @@ __device__ __forceinline__ float row_sum(float v, float *s, int warp, uint32_t l
         v = 0.0f;
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            v += s[warp / W * W + i];
+            v += s[i];
     }
     return v;
 }
+__device__ __forceinline__ float rstd_of(float sum, float inv_k, float eps)
+{
+    return rsqrtf(fmaf(sum, inv_k, eps));
+}
+
+// h' of 8 values of h and y; into y.
+__device__ __forceinline__ void update(const Post &c, float res_scale, float rstd, const uint32_t (&h)[4],
+                                       uint32_t (&y)[4])
+{
+    const float2 r2 = make_float2(rstd, rstd), s2 = make_float2(res_scale, res_scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 u = __fmul2_rn(__fmul2_rn(pair_of(y[i]), r2), c.post[i]);
+        u = __ffma2_rn(s2, pair_of(h[i]), u);
+        y[i] = pack_bf16x2(u.x, u.y);
+    }
+}
+
+// n of 8 values of h'.
+__device__ __forceinline__ void normalise(const Pre &c, float rstd, const uint32_t (&h)[4], uint32_t (&n)[4])
+{
+    const float2 r2 = make_float2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = __ffma2_rn(__fmul2_rn(pair_of(h[i]), r2), c.pre[i], c.shift[i]);
+        n[i] = pack_bf16x2(a.x, a.y);
+    }
+}
+
+// ------------------------------------------------------------------ many rows
+// Shared memory: the ring, `stages` slots of h and y of a row (4 K bytes), then this.
 template <int W>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, float *s, int warp, uint32_t lane)
-{
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if (W > 1) {
-        if (lane == 0)
-            s[warp] = __uint_as_float(v);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            v = max(v, __float_as_uint(s[warp / W * W + i]));
-    }
-    return v;
-}
+struct StreamTail {
+    float red[2][2][W];                  // by row parity and sum
+    uint32_t top[2][W];
+    uint64_t full[fp4::kMaxRing];
+    int abort;
+};
 
-__device__ __forceinline__ float rstd_of(float sum, int64_t K, float eps)
-{
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(K)), eps)));
-}
+constexpr int kStreamWarps = 16;         // warps a SM (128 registers a thread)
 
-// h' of V values.
-template <int V>
-__device__ __forceinline__ void update(const Params &p, const uint32_t (&h)[V / 2], const uint32_t (&y)[V / 2],
-                                       float rstd, int64_t col, int64_t mod, uint32_t (&o)[V / 2])
+template <int kOut, int W, int P>
+__global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_kernel(const Params p)
 {
-    uint32_t pg[V / 2], g[V / 2];
-    if (p.post_gamma != nullptr)
-        load_col<V>(p.post_gamma + col, pg);
-    if (p.gate != nullptr)
-        load_col<V>(p.gate + mod + col, g);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        float u0 = __fmul_rn(bf16_lo(y[i]), rstd), u1 = __fmul_rn(bf16_hi(y[i]), rstd);
-        if (p.post_gamma != nullptr) {
-            u0 = __fmul_rn(u0, bf16_lo(pg[i]));
-            u1 = __fmul_rn(u1, bf16_hi(pg[i]));
-        }
-        if (p.gate != nullptr) {
-            u0 = __fmul_rn(u0, bf16_lo(g[i]));
-            u1 = __fmul_rn(u1, bf16_hi(g[i]));
-        }
-        o[i] = pack_bf16x2(__fmaf_rn(p.res_scale, bf16_lo(h[i]), u0), __fmaf_rn(p.res_scale, bf16_hi(h[i]), u1));
-    }
-}
-
-// n of V values of h'.
-template <int V>
-__device__ __forceinline__ void normalise(const Params &p, const uint32_t (&h)[V / 2], float rstd, int64_t col,
-                                          int64_t mod, uint32_t (&o)[V / 2])
-{
-    uint32_t g[V / 2], sc[V / 2], sh[V / 2];
-    if (p.pre_gamma != nullptr)
-        load_col<V>(p.pre_gamma + col, g);
-    if (p.scale != nullptr)
-        load_col<V>(p.scale + mod + col, sc);
-    if (p.shift != nullptr)
-        load_col<V>(p.shift + mod + col, sh);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        float a = __fmul_rn(bf16_lo(h[i]), rstd), b = __fmul_rn(bf16_hi(h[i]), rstd);
-        if (p.pre_gamma != nullptr) {
-            a = __fmul_rn(a, bf16_lo(g[i]));
-            b = __fmul_rn(b, bf16_hi(g[i]));
-        }
-        if (p.scale != nullptr) {
-            a = __fmul_rn(a, __fadd_rn(1.0f, bf16_lo(sc[i])));
-            b = __fmul_rn(b, __fadd_rn(1.0f, bf16_hi(sc[i])));
-        }
-        if (p.shift != nullptr) {
-            a = __fadd_rn(a, bf16_lo(sh[i]));
-            b = __fadd_rn(b, bf16_hi(sh[i]));
-        }
-        o[i] = pack_bf16x2(a, b);
-    }
-}
-
-// kOut: BF16 or a 4-bit format (V = 16).  A row of at most 32 V W P values stays in registers;
-// a longer one is read again for each of its passes (kLong).
-template <int kOut, int V, int W, int P, bool kLong>
-__global__ void __launch_bounds__(kWarps * 32) block_norm_kernel(const Params p)
-{
-    static_assert(kOut == kOutBf16 || V == 16, "a lane encodes 16 values");
-    __shared__ float s_red[3][kWarps];
+    extern __shared__ __align__(128) uint8_t ring[];
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2;
+    const int S = p.stages;
+    StreamTail<W> &sm = *reinterpret_cast<StreamTail<W> *>(ring + static_cast<size_t>(S) * 2 * row_bytes);
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
-    const bool live = r < p.M;
-    const int64_t np = live ? p.K / V : 0;       // pieces of the row
-    const int64_t b0 = (warp % W) * 32 + lane;
-    constexpr int64_t kStep = W * 32;
-    constexpr int64_t kChunk = kStep * P;
-    const int64_t at = r * p.K;
-    const int64_t mod = live ? r / p.T * p.K : 0;
-    uint32_t h[P][V / 2], y[P][V / 2];           // y becomes h', h becomes n
+    const int np = static_cast<int>(p.K / 8);
+    const int b0 = warp * 32 + static_cast<int>(lane);
+    const int64_t KT = kOut == kOutBf16 ? 0 : fp4::scale_tiles(p.K, kOut);
+    constexpr int kStep = W * 32;
+    volatile int *abort = &sm.abort;
 
-    // the branch's sum of squares
-    float rstd = 1.0f, sum = 0.0f;
-    for (int64_t c = 0; c < np; c += kChunk) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int64_t b = b0 + c + i * kStep;
-            if (b < np) {
-                load_row<V>(p.y + at + b * V, y[i]);
-                if (!kLong)
-                    load_row<V>(p.h + at + b * V, h[i]);
-            }
-        }
-        if (!p.post_norm)
-            continue;
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (b0 + c + i * kStep < np)
-                sum += squares<V>(y[i]);
+    auto fetch = [&](int64_t r, int s) {
+        uint8_t *slot = ring + static_cast<size_t>(s) * 2 * row_bytes;
+        mbar_arrive_expect_tx(&sm.full[s], 2 * row_bytes);
+        fp4::bulk_load(slot, p.y + r * p.K, row_bytes, &sm.full[s]);
+        fp4::bulk_load(slot + row_bytes, p.h + r * p.K, row_bytes, &sm.full[s]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s)
+            mbar_init(&sm.full[s], 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        int64_t r = blockIdx.x;
+        for (int s = 0; s < S && r < p.M; ++s, r += gridDim.x)
+            fetch(r, s);
     }
-    if (p.post_norm)
-        rstd = rstd_of(row_sum<W>(sum, s_red[0], warp, lane), p.K, p.eps);
+    __syncthreads();
 
-    // h', and its sum of squares
-    sum = 0.0f;
-    for (int64_t c = 0; c < np; c += kChunk) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int64_t b = b0 + c + i * kStep;
-            if (b < np) {
-                if (kLong) {
-                    load_row<V>(p.y + at + b * V, y[i]);
-                    load_row<V>(p.h + at + b * V, h[i]);
-                }
-                uint32_t o[V / 2];
-                update<V>(p, h[i], y[i], rstd, b * V, mod, o);
-                store_row<V>(p.h_out + at + b * V, o);
-                sum += squares<V>(o);
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j)
-                    y[i][j] = o[j];
-            }
-        }
-    }
-    rstd = rstd_of(row_sum<W>(sum, s_red[1], warp, lane), p.K, p.eps);
-
-    // n, and for kNv its largest magnitude
-    fp4::Row row{};
-    uint32_t top = 0;
-    if (kOut == kOutBf16 || kOut == fp4::kNv || !kLong) {
-        for (int64_t c = 0; c < np; c += kChunk) {
+    constexpr bool kKeep = P <= 2;
+    Post post[kKeep ? P : 1];
+    Pre pre[kKeep ? P : 1];
+    const float inv_k = __fdiv_rn(1.0f, static_cast<float>(p.K));
+    int64_t group = -1;
+    int s = 0, par = 0;
+    uint32_t phase = 0;
+    for (int64_t r = blockIdx.x; r < p.M; r += gridDim.x, par ^= 1) {
+        const int64_t g = r / p.T;
+        if (kKeep && g != group) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int64_t b = b0 + c + i * kStep;
+                const int b = b0 + i * kStep;
                 if (b < np) {
-                    if (kLong)
-                        load_row<V>(p.h_out + at + b * V, y[i]);
-                    normalise<V>(p, y[i], rstd, b * V, mod, h[i]);
-                    if constexpr (kOut == kOutBf16)
-                        store_row<V>(p.n_out + at + b * V, h[i]);
-                    else
-                        top = max(top, fp4::amax16(h[i]));
+                    load_post(p, b * 8, g * p.K, post[kKeep ? i : 0]);
+                    load_pre(p, b * 8, g * p.K, pre[kKeep ? i : 0]);
                 }
+            }
+        }
+        group = g;
+        // A wait that gives up is recorded; the row is then worked on as it is, so that every
+        // warp reaches every barrier.
+        mbar_wait(&sm.full[s], phase, abort);
+        const uint8_t *slot = ring + static_cast<size_t>(s) * 2 * row_bytes;
+        uint32_t y[P][4], h[P][4];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + i * kStep;
+            y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0;
+            h[i][0] = h[i][1] = h[i][2] = h[i][3] = 0;
+            if (b < np) {
+                unpack4(ld_shared_v4(slot + b * 16), y[i]);
+                unpack4(ld_shared_v4(slot + row_bytes + b * 16), h[i]);
+            }
+        }
+        uint16_t *h_row = p.h_out + r * p.K;
+        float rstd = 1.0f;
+        if (p.post_norm) {
+            float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                add_squares(y[i], acc);
+            rstd = rstd_of(row_sum<W>(acc.x + acc.y, sm.red[par][0], warp, lane), inv_k, p.eps);
+        }
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + i * kStep;
+            if (b < np) {
+                Post &f = post[kKeep ? i : 0];
+                if (!kKeep)
+                    load_post(p, b * 8, g * p.K, f);
+                update(f, p.res_scale, rstd, h[i], y[i]);
+                *reinterpret_cast<uint4 *>(h_row + b * 8) = pack4(y[i]);
+                add_squares(y[i], acc);
+            }
+        }
+        if (W == 1)
+            __syncwarp();
+        rstd = rstd_of(row_sum<W>(acc.x + acc.y, sm.red[par][1], warp, lane), inv_k, p.eps);
+        // every thread has read the slot
+        if (threadIdx.x == 0 && r + static_cast<int64_t>(S) * gridDim.x < p.M)
+            fetch(r + static_cast<int64_t>(S) * gridDim.x, s);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + i * kStep;
+            if (b < np) {
+                Pre &f = pre[kKeep ? i : 0];
+                if (!kKeep)
+                    load_pre(p, b * 8, g * p.K, f);
+                normalise(f, rstd, y[i], h[i]);
+                if constexpr (kOut == kOutBf16)
+                    *reinterpret_cast<uint4 *>(p.n_out + r * p.K + b * 8) = pack4(h[i]);
+                else
+                    top = max(top, fp4::amax8(h[i]));
+            }
+        }
+        if constexpr (kOut != kOutBf16) {
+            fp4::Row row{};
+            if (kOut == fp4::kNv) {
+                row = fp4::row_of(fp4::row_top<W>(top, sm.top[par], warp, lane));
+                if (threadIdx.x == 0)
+                    p.factor[r] = row.factor;
+            }
+            uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + fp4::scale_row(r, KT);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int b = b0 + i * kStep;
+                fp4::store_piece<kOut>(codes, scales, b, b < np, fp4::pieces_padded<kOut>(KT), row, h[i]);
+            }
+        }
+        if (++s == S) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if constexpr (kOut != kOutBf16)
+        fp4::zero_scales(p.scales, p.M, p.M_pad, KT, blockIdx.x, gridDim.x);
+}
+
+// ------------------------------------------------------------------ few or long rows
+// A row of at most 256 W P values stays in registers; a longer one is read again for each of
+// its passes (kLong).  One row a CTA.
+template <int kOut, int W, int P, bool kLong>
+__global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
+{
+    __shared__ float s_red[2][W];
+    __shared__ uint32_t s_top[W];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const int64_t r = blockIdx.x;
+    if (kOut != kOutBf16 && r >= p.M) {          // CTAs past the last row clear its tile's scales
+        fp4::zero_scales(p.scales, r, r + 1, fp4::scale_tiles(p.K, kOut), 0, 1);
+        return;
+    }
+    const int np = static_cast<int>(p.K / 8);
+    const int b0 = warp * 32 + static_cast<int>(lane);
+    constexpr int kStep = W * 32;
+    constexpr int kChunk = kStep * P;
+    const int64_t at = r * p.K;
+    const int64_t mod = r / p.T * p.K;
+    uint32_t h[P][4], y[P][4];
+    // factors of up to two pieces are loaded with the row, ahead of the first reduction
+    constexpr bool kAhead = !kLong && P <= 2;
+    Post post[kAhead ? P : 1];
+    Pre pre[kAhead ? P : 1];
+    const float inv_k = __fdiv_rn(1.0f, static_cast<float>(p.K));
+
+    // the branch's sum of squares
+    float rstd = 1.0f;
+    float2 acc = make_float2(0.0f, 0.0f);
+    for (int at_c = 0; at_c < np; at_c += kChunk) {
+        if (kLong && !p.post_norm)
+            break;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + at_c + i * kStep;
+            y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0;
+            if (b < np) {
+                unpack4(*reinterpret_cast<const uint4 *>(p.y + at + static_cast<size_t>(b) * 8), y[i]);
+                if (!kLong) {
+                    unpack4(*reinterpret_cast<const uint4 *>(p.h + at + static_cast<size_t>(b) * 8), h[i]);
+                }
+                if (kAhead) {
+                    load_post(p, int64_t{8} * b, mod, post[kAhead ? i : 0]);
+                    load_pre(p, int64_t{8} * b, mod, pre[kAhead ? i : 0]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            add_squares(y[i], acc);
+    }
+    if (p.post_norm)
+        rstd = rstd_of(row_sum<W>(acc.x + acc.y, s_red[0], warp, lane), inv_k, p.eps);
+
+    // h', and its sum of squares
+    acc = make_float2(0.0f, 0.0f);
+    for (int at_c = 0; at_c < np; at_c += kChunk) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + at_c + i * kStep;
+            if (b < np) {
+                if (kLong) {
+                    unpack4(*reinterpret_cast<const uint4 *>(p.y + at + static_cast<size_t>(b) * 8), y[i]);
+                    unpack4(*reinterpret_cast<const uint4 *>(p.h + at + static_cast<size_t>(b) * 8), h[i]);
+                }
+                Post &f = post[kAhead ? i : 0];
+                if (!kAhead)
+                    load_post(p, int64_t{8} * b, mod, f);
+                update(f, p.res_scale, rstd, h[i], y[i]);
+                *reinterpret_cast<uint4 *>(p.h_out + at + static_cast<size_t>(b) * 8) = pack4(y[i]);
+                add_squares(y[i], acc);
+            }
+        }
+    }
+    rstd = rstd_of(row_sum<W>(acc.x + acc.y, s_red[1], warp, lane), inv_k, p.eps);
+
+    // n, and for kNv its largest magnitude; a long row's n is formed again for its codes
+    uint32_t top = 0;
+    for (int at_c = 0; at_c < (kLong && kOut == fp4::kMx ? 0 : np); at_c += kChunk) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + at_c + i * kStep;
+            if (b < np) {
+                if (kLong)
+                    unpack4(*reinterpret_cast<const uint4 *>(p.h_out + at + static_cast<size_t>(b) * 8), y[i]);
+                Pre &f = pre[kAhead ? i : 0];
+                if (!kAhead)
+                    load_pre(p, int64_t{8} * b, mod, f);
+                normalise(f, rstd, y[i], h[i]);
+                if constexpr (kOut == kOutBf16)
+                    *reinterpret_cast<uint4 *>(p.n_out + at + static_cast<size_t>(b) * 8) = pack4(h[i]);
+                else
+                    top = max(top, fp4::amax8(h[i]));
             }
         }
     }
     if constexpr (kOut != kOutBf16) {
+        fp4::Row row{};
         if (kOut == fp4::kNv) {
-            row = fp4::row_of(row_max<W>(top, s_red[2], warp, lane));
-            if (live && b0 == 0)
+            row = fp4::row_of(fp4::row_top<W>(top, s_top, warp, lane));
+            if (threadIdx.x == 0)
                 p.factor[r] = row.factor;
         }
-        if (r >= p.M_pad)
-            return;
         const int64_t KT = fp4::scale_tiles(p.K, kOut);
-        constexpr int kPer = kOut == fp4::kNv ? 4 : 8;
-        const int64_t nb_pad = KT * kPer;
-        for (int64_t c = 0; c < nb_pad; c += kChunk) {
+        const int np_pad = fp4::pieces_padded<kOut>(KT);
+        uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + fp4::scale_row(r, KT);
+        for (int at_c = 0; at_c < np_pad; at_c += kChunk) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int64_t b = b0 + c + i * kStep;
-                const bool in = b < np;
-                if (kLong && in) {
-                    load_row<V>(p.h_out + at + b * V, y[i]);
-                    normalise<V>(p, y[i], rstd, b * V, mod, h[i]);
+                const int b = b0 + at_c + i * kStep;
+                if (kLong && b < np) {
+                    unpack4(*reinterpret_cast<const uint4 *>(p.h_out + at + static_cast<size_t>(b) * 8), y[i]);
+                    load_pre(p, int64_t{8} * b, mod, pre[0]);
+                    normalise(pre[0], rstd, y[i], h[i]);
                 }
-                uint32_t m = in ? fp4::amax16(h[i]) : 0;
-                if (kOut == fp4::kMx)
-                    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                uint32_t byte = 0;
-                if (in) {
-                    const uint2 o = fp4::encode16<kOut>(h[i], m, row, byte);
-                    *reinterpret_cast<uint2 *>(p.codes + r * (p.K / 2) + b * 8) = o;
-                }
-                const uint32_t word = fp4::gather_scales<kOut>(byte);
-                if (b < nb_pad && fp4::stores_scales<kOut>(b))
-                    *reinterpret_cast<uint32_t *>(p.scales + fp4::scale_word(r, b / kPer, KT)) = word;
+                fp4::store_piece<kOut>(codes, scales, b, b < np, np_pad, row, h[i]);
             }
         }
     }

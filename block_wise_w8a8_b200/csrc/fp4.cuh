@@ -17,15 +17,15 @@
 // block use E4M3's whole range whatever the row's size; it depends on no other row, so a
 // row's codes are the same in every batch.
 //
-// Both formats' quotients are taken exactly as written, although no element is divided:
+// Both formats' quotients are taken exactly as written, although nothing is divided:
 //   kMx  v 2^-e is exact in FP32.
-//   kNv  448 amax and A have 11 and 8 significant bits: their IEEE quotient is an E4M3
-//        rounding boundary only if the exact one is.  For the codes, 2688 v has 13 bits and
-//        s A 12.  A boundary of E2M1 is j 2^i with odd j <= 7, so a quotient off the
-//        boundary is off by 2^-14.9 of itself at least (two different whole numbers, the
-//        larger below 7 * 2^12, differ by one).  v * fl(0.65625 * fl(1 / (s A / 4096)))
-//        is within 2^-22 of the quotient; rounded to 17 significant bits it lies on a
-//        boundary only if the quotient does, and on the same side of it otherwise.
+//   kNv  448 amax has 11 significant bits, A 8; 2688 v has 13 and s A 12.  A rounding
+//        boundary of E4M3 is j 2^i with odd j < 32, of E2M1 with odd j <= 7, so a quotient
+//        off the boundary is off by 2^-13 (scale) or 2^-14.9 (code) of itself at least: two
+//        different whole numbers, the larger below 32 * 2^8 or 7 * 2^12, differ by one.  The
+//        products with reciprocals below are within 2^-21 of the quotients (four roundings
+//        and a reciprocal good to one unit in the last place).  Rounded to 17 significant bits they
+//        lie on a boundary only if the quotient does, and on the same side of it otherwise.
 //
 // Scales lie as tcgen05 block-scaled products read them: 512-byte tiles of 128 rows x 4
 // scales along K, tile [row / 128][block / 4], byte 16 (row % 32) + 4 (row % 128 / 32) +
@@ -49,13 +49,13 @@ __host__ __device__ constexpr int64_t scale_tiles(int64_t K, int fmt)
     return fmt == kMx ? (K + 127) / 128 : (K + 63) / 64;
 }
 
-// Byte offset, inside its tile, of the four scales of row r.
-__device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kt, int64_t KT)
+// Byte offset of row r's first four scales; the next four are 512 bytes on.
+__device__ __forceinline__ int64_t scale_row(int64_t r, int64_t KT)
 {
-    return ((r >> 7) * KT + kt) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+    return (r >> 7) * KT * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
-// Two FP32 numbers -> two E2M1 codes in the low byte, the first in its low half.
+// Eight FP32 numbers -> eight E2M1 codes, the first in the lowest four bits.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])
 {
     uint32_t o;
@@ -99,36 +99,62 @@ __device__ __forceinline__ float from_e4m3(uint32_t byte)
     return f;
 }
 
-// Largest BF16 magnitude pattern among 8 packed words (16 values), in the low 16 bits.
-__device__ __forceinline__ uint32_t amax16(const uint32_t (&w)[8])
+// a rounded to 17 significant bits, and 1 / a to one unit in the last place (a normal, > 0).
+__device__ __forceinline__ float round17(float a)
 {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return __uint_as_float((__float_as_uint(a) + 0x40u) & ~0x7Fu);
+}
+__device__ __forceinline__ float reciprocal(float a)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+
+// Largest BF16 magnitude pattern among 8 values (4 packed words), in the low 16 bits.
+__device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[4])
+{
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
     return max(m & 0xFFFFu, m >> 16);
 }
 
 // What a row's factor and its blocks' scales are taken from (kNv), given the row's largest
 // magnitude pattern.
 struct Row {
-    float top;        // A; unused for kMx
-    float factor;     // what is stored; unused for kMx
-    bool bad;         // the row holds an infinity or a NaN (kNv)
+    float to_scale;   // 448 / A; unused for kMx, like the rest
+    float to_code;    // 2688 / A
+    float factor;     // what is stored
+    bool bad;         // the row holds an infinity or a NaN
 };
 __device__ __forceinline__ Row row_of(uint32_t amax_bits)
 {
     Row r;
     r.bad = amax_bits >= 0x7F80u;
-    r.top = r.bad ? 1.0f : fmaxf(__uint_as_float(amax_bits << 16), kTiny);
-    r.factor = r.bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(r.top, kRowDiv);
+    const float top = r.bad ? 1.0f : fmaxf(__uint_as_float(amax_bits << 16), kTiny);
+    r.factor = r.bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(top, kRowDiv);
+    r.to_scale = __fdiv_rn(448.0f, top);
+    r.to_code = __fdiv_rn(kRowDiv, top);
     return r;
 }
 
-// Codes of 16 values (8 packed BF16 pairs) and the scale byte of their block; for kMx the
-// magnitude pattern `m` is that of all 32 values of the block (two lanes hold them).
+// A lane holds 8 consecutive values (so that a warp's loads and stores are 512 contiguous
+// bytes); 2 (kNv) or 4 (kMx) neighbouring lanes share a block.  Lane order = order along K.
 template <int kFmt>
-__device__ __forceinline__ uint2 encode16(const uint32_t (&w)[8], uint32_t m, const Row &row, uint32_t &byte)
+constexpr int kBlockLanes = kFmt == kMx ? 4 : 2;
+
+// The largest magnitude of the lane's block, from its own values'.
+template <int kFmt>
+__device__ __forceinline__ uint32_t block_amax(uint32_t m)
+{
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    return kFmt == kMx ? max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) : m;
+}
+
+// Codes of 8 values (4 packed BF16 pairs) and the scale byte of their block, given the
+// block's largest magnitude pattern.
+template <int kFmt>
+__device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], uint32_t m, const Row &row, uint32_t &byte)
 {
     float mult;
     bool zero;
@@ -138,49 +164,78 @@ __device__ __forceinline__ uint2 encode16(const uint32_t (&w)[8], uint32_t m, co
         byte = zero ? 255u : (e > 2u ? e - 2u : 0u);
         mult = zero ? 0.0f : __uint_as_float((254u - byte) << 23);
     } else {
-        byte = row.bad ? 0u : to_e4m3(__fdiv_rn(__uint_as_float(m << 16) * 448.0f, row.top));
         zero = row.bad;
-        const float unit = from_e4m3(byte) * (row.top * (1.0f / 4096.0f));
-        mult = byte == 0u ? 0.0f : 0.65625f * __frcp_rn(unit);
+        byte = zero ? 0u : to_e4m3(round17(__uint_as_float(m << 16) * row.to_scale));
+        mult = byte == 0u ? 0.0f : row.to_code * reciprocal(from_e4m3(byte));
     }
-    uint2 o;
+    float v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(w[4 * h + i]) * mult;
-            v[2 * i + 1] = bf16_hi(w[4 * h + i]) * mult;
-        }
-        if (kFmt == kNv) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)                  // 17 significant bits
-                v[i] = __uint_as_float((__float_as_uint(v[i]) + 0x40u) & ~0x7Fu);
-        }
-        const uint32_t c = zero ? 0u : e2m1x8(v);
-        if (h == 0)
-            o.x = c;
-        else
-            o.y = c;
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = __fmul2_rn(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), make_float2(mult, mult));
+        v[2 * i] = kFmt == kNv ? round17(q.x) : q.x;
+        v[2 * i + 1] = kFmt == kNv ? round17(q.y) : q.y;
     }
-    return o;
+    return zero ? 0u : e2m1x8(v);
 }
 
-// One scale byte a lane (each lane holds 16 consecutive values, lane order = order along
-// K) -> the four scales of a tile's row in one word, on the lanes that store it: every
-// fourth lane (kNv), every eighth (kMx, where two lanes share a block).
+// Scale bytes, one a block's lanes -> the four scales of a tile's row in one word, on the
+// lane that stores it: every eighth (kNv) or sixteenth (kMx).
 template <int kFmt>
 __device__ __forceinline__ uint32_t gather_scales(uint32_t byte)
 {
     constexpr uint32_t kFull = 0xFFFFFFFFu;
-    constexpr int step = kFmt == kNv ? 1 : 2;
+    constexpr int step = kBlockLanes<kFmt>;
     uint32_t v = byte | (__shfl_down_sync(kFull, byte, step) << 8);
     return v | (__shfl_down_sync(kFull, v, 2 * step) << 16);
 }
+// Whether piece b of 8 values is the first of a scale word, and which tile along K it is in.
 template <int kFmt>
-__device__ __forceinline__ bool stores_scales(int64_t block16)
+__device__ __forceinline__ bool stores_scales(int b)
 {
-    return (block16 & (kFmt == kNv ? 3 : 7)) == 0;
+    return (b & (4 * kBlockLanes<kFmt> - 1)) == 0;
+}
+template <int kFmt>
+__device__ __forceinline__ int scale_tile(int b)
+{
+    return b / (4 * kBlockLanes<kFmt>);
+}
+
+// Codes of a lane's piece b (of np) of a row, and the scales of the 4 blocks around it; every
+// lane of the warp takes part, `in` (b < np) or not.  codes and scales: the row's.
+template <int kFmt>
+__device__ __forceinline__ void store_piece(uint8_t *codes, uint8_t *scales, int b, bool in, int np_pad, const Row &row,
+                                            const uint32_t (&w)[4])
+{
+    const uint32_t m = block_amax<kFmt>(in ? amax8(w) : 0);
+    uint32_t byte = 0;
+    if (in)
+        *reinterpret_cast<uint32_t *>(codes + static_cast<uint32_t>(b) * 4) = encode8<kFmt>(w, m, row, byte);
+    const uint32_t word = gather_scales<kFmt>(byte);
+    if (stores_scales<kFmt>(b) && b < np_pad)
+        *reinterpret_cast<uint32_t *>(scales + static_cast<size_t>(scale_tile<kFmt>(b)) * 512) = word;
+}
+// Pieces of 8 values of a row with its last scale tile filled up.
+template <int kFmt>
+__device__ __forceinline__ int pieces_padded(int64_t KT)
+{
+    return static_cast<int>(KT) * 4 * kBlockLanes<kFmt>;
+}
+
+// Largest magnitude pattern over the W warps of a row (s[W], if W > 1 in shared memory); every
+// thread of the row takes part.
+template <int W>
+__device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *s, int warp, uint32_t lane)
+{
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    if (W > 1) {
+        if (lane == 0)
+            s[warp] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            v = max(v, s[i]);
+    }
+    return v;
 }
 
 struct QParams {
@@ -192,95 +247,178 @@ struct QParams {
     float *factor;           // [rows] (kNv)
 };
 
-__device__ __forceinline__ void load16(const uint16_t *p, uint32_t (&w)[8])
+__device__ __forceinline__ void load8(const uint16_t *p, uint32_t (&w)[4])
 {
     const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// W warps share a row; a lane holds up to P pieces of 16 values of it in registers, so the
-// row is read once when K <= 512 W P (longer rows are read again, from L2, for the codes).
-template <int kFmt, int W, int P>
-__global__ void __launch_bounds__(kWarps * 32) quantize_kernel(const QParams p)
+// Scales of rows past the end: zeros, by CTA `cta` of `ctas`.
+__device__ __forceinline__ void zero_scales(uint8_t *scales, int64_t rows, int64_t rows_pad, int64_t KT, int64_t cta,
+                                            int64_t ctas)
 {
-    __shared__ uint32_t s_top[kWarps];
+    for (int64_t r = rows + cta; r < rows_pad; r += ctas)
+        for (int64_t t = threadIdx.x; t < KT; t += blockDim.x)
+            *reinterpret_cast<uint32_t *>(scales + scale_row(r, KT) + t * 512) = 0;
+}
+
+// Few rows, or rows too long for the ring below.  W warps, one row; a lane holds up to P
+// pieces of 8 values in registers, so the row is read once when K <= 256 W P (longer rows are
+// read again, from L2, for the codes).  CTAs past the last row clear its tile's scales.
+template <int kFmt, int W, int P>
+__global__ void __launch_bounds__(W * 32) quantize_kernel(const QParams p)
+{
+    __shared__ uint32_t s_top[W];
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
-    const int lane = static_cast<int>(lane_id());
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
-    const int64_t nb = p.K / 16;
+    const uint32_t lane = lane_id();
+    const int64_t r = blockIdx.x;
+    const int np = static_cast<int>(p.K / 8);
     const int64_t KT = scale_tiles(p.K, kFmt);
-    const int64_t nb_pad = KT * (kFmt == kNv ? 4 : 8);
-    const int64_t b0 = (warp % W) * 32 + lane;
-    constexpr int64_t kStep = W * 32;
-    const bool live = r < p.rows;
+    if (r >= p.rows) {
+        zero_scales(p.scales, r, r + 1, KT, 0, 1);
+        return;
+    }
+    const int np_pad = pieces_padded<kFmt>(KT);
+    const int b0 = warp * 32 + static_cast<int>(lane);
+    constexpr int kStep = W * 32;
     const uint16_t *xr = p.x + r * p.K;
-    uint32_t w[P][8];
-    uint32_t m[P];
+    uint32_t w[P][4];
     uint32_t top = 0;
-    const bool once = nb <= kStep * P;
-    if (live && (kFmt == kNv || once)) {
-        for (int64_t c = 0; c < nb; c += kStep * P) {
+    const bool once = np <= kStep * P;
+    if (kFmt == kNv || once) {
+        for (int c = 0; c < np; c += kStep * P) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int64_t b = b0 + c + i * kStep;
-                if (b < nb)
-                    load16(xr + b * 16, w[i]);
-            }
+            for (int i = 0; i < P; ++i)
+                if (b0 + c + i * kStep < np)
+                    load8(xr + static_cast<size_t>(b0 + c + i * kStep) * 8, w[i]);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int64_t b = b0 + c + i * kStep;
-                m[i] = b < nb ? amax16(w[i]) : 0;
-                top = max(top, m[i]);
-            }
+            for (int i = 0; i < P; ++i)
+                if (kFmt == kNv && b0 + c + i * kStep < np)
+                    top = max(top, amax8(w[i]));
         }
     }
     Row row{};
     if (kFmt == kNv) {
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (W > 1) {
-            if (lane == 0)
-                s_top[warp] = top;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                top = max(top, s_top[warp / W * W + i]);
-        }
-        row = row_of(top);
-        if (live && b0 == 0)
+        row = row_of(row_top<W>(top, s_top, warp, lane));
+        if (threadIdx.x == 0)
             p.factor[r] = row.factor;
     }
-    if (r >= p.rows_pad)
-        return;
-    for (int64_t c = 0; c < nb_pad; c += kStep * P) {
+    uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
+    for (int c = 0; c < np_pad; c += kStep * P) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int64_t b = b0 + c + i * kStep;
-            const bool in = live && b < nb;
-            if (!once && in) {
-                load16(xr + b * 16, w[i]);
-                m[i] = amax16(w[i]);
-            }
-            uint32_t mm = in ? m[i] : 0;
-            if (kFmt == kMx)
-                mm = max(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 1));
-            uint32_t byte = 0;
-            if (in) {
-                const uint2 o = encode16<kFmt>(w[i], mm, row, byte);
-                *reinterpret_cast<uint2 *>(p.codes + r * (p.K / 2) + b * 8) = o;
-            }
-            const uint32_t word = gather_scales<kFmt>(byte);
-            if (b < nb_pad && stores_scales<kFmt>(b))
-                *reinterpret_cast<uint32_t *>(p.scales + scale_word(r, b / (kFmt == kNv ? 4 : 8), KT)) = word;
+            const int b = b0 + c + i * kStep;
+            if (!once && b < np)
+                load8(xr + static_cast<size_t>(b) * 8, w[i]);
+            store_piece<kFmt>(codes, scales, b, b < np, np_pad, row, w[i]);
         }
     }
 }
 
+// Bytes into shared memory, completion counted on `bar`; 16-byte aligned, whole 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Many rows.  CTAs of W warps stay, take every gridDim.x-th row, and have the next rows copied
+// into a ring in shared memory (a bulk copy each) while they code: with a CTA a row the loads,
+// the arithmetic and the stores of the few CTAs that fit a SM hardly overlap (16384 x 4096
+// nvfp4: 49 us).  A lane has up to 4 pieces of 8 values, K <= 1024 W.
+constexpr int kStreamPieces = 4;
+constexpr int kStreamWarps = 32;                 // warps a SM
+constexpr int kMaxRing = 16;                     // rows of a ring at most
+template <int W>
+struct StreamTail {                              // behind the ring
+    uint32_t top[2][W];                          // by row parity
+    uint64_t full[kMaxRing];
+    int abort;
+};
+
+template <int kFmt, int W>
+__global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kernel(const QParams p, const int stages)
+{
+    constexpr int P = kStreamPieces;
+    extern __shared__ __align__(128) uint8_t ring[];
+    const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2;
+    StreamTail<W> &sm = *reinterpret_cast<StreamTail<W> *>(ring + static_cast<size_t>(stages) * row_bytes);
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const int np = static_cast<int>(p.K / 8);
+    const int64_t KT = scale_tiles(p.K, kFmt);
+    const int np_pad = pieces_padded<kFmt>(KT);
+    const int b0 = warp * 32 + static_cast<int>(lane);
+    constexpr int kStep = W * 32;
+    volatile int *abort = &sm.abort;
+
+    auto fetch = [&](int64_t r, int s) {
+        mbar_arrive_expect_tx(&sm.full[s], row_bytes);
+        bulk_load(ring + static_cast<size_t>(s) * row_bytes, p.x + r * p.K, row_bytes, &sm.full[s]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s)
+            mbar_init(&sm.full[s], 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        int64_t r = blockIdx.x;
+        for (int s = 0; s < stages && r < p.rows; ++s, r += gridDim.x)
+            fetch(r, s);
+    }
+    __syncthreads();
+    int s = 0, par = 0;
+    uint32_t phase = 0;
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, par ^= 1) {
+        // A wait that gives up is recorded; the row is then coded as it is, so that every warp
+        // reaches every barrier.
+        mbar_wait(&sm.full[s], phase, abort);
+        const uint8_t *slot = ring + static_cast<size_t>(s) * row_bytes;
+        uint32_t w[P][4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+            if (b0 + i * kStep < np) {
+                const uint4 v = ld_shared_v4(slot + (b0 + i * kStep) * 16);
+                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+            }
+        }
+        Row row{};
+        if (kFmt == kNv) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                top = max(top, amax8(w[i]));
+            row = row_of(row_top<W>(top, sm.top[par], warp, lane));
+            if (threadIdx.x == 0)
+                p.factor[r] = row.factor;
+        } else if (W > 1) {
+            __syncthreads();
+        }
+        if (W == 1)
+            __syncwarp();
+        // every thread has read the slot
+        if (threadIdx.x == 0 && r + static_cast<int64_t>(stages) * gridDim.x < p.rows)
+            fetch(r + static_cast<int64_t>(stages) * gridDim.x, s);
+        uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (i * kStep < np_pad)
+                store_piece<kFmt>(codes, scales, b0 + i * kStep, b0 + i * kStep < np, np_pad, row, w[i]);
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    zero_scales(p.scales, p.rows, p.rows_pad, KT, blockIdx.x, gridDim.x);
+}
+
 // y [rows, K] BF16 = the values the codes stand for: fl(code * scale) is exact, the product
-// with the row factor is rounded to FP32, the result once more to BF16.  A lane takes 16
-// values; a warp 512 consecutive ones of a row.
+// with the row factor is rounded to FP32, the result once more to BF16.  A lane takes 8
+// values; a warp kDeqPieces runs of 256 consecutive ones of a row.
 struct DParams {
     const uint8_t *codes;
     const uint8_t *scales;
@@ -288,48 +426,52 @@ struct DParams {
     int64_t rows, K;
     uint16_t *y;
 };
+constexpr int kDeqPieces = 4;
 
 template <int kFmt>
 __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const DParams p)
 {
     const int lane = static_cast<int>(lane_id());
-    const int64_t nb = p.K / 16;
-    const int64_t per_row = (nb + 31) / 32;
+    const int64_t np = p.K / 8;
+    const int64_t per_row = (np + 32 * kDeqPieces - 1) / (32 * kDeqPieces);
     const int64_t KT = scale_tiles(p.K, kFmt);
-    const int64_t total = p.rows * per_row;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (g >= total)
+    if (g >= p.rows * per_row)
         return;
     const int64_t r = g / per_row;
-    const int64_t b = (g - r * per_row) * 32 + lane;
-    if (b >= nb)
-        return;
-    const uint2 c = __ldg(reinterpret_cast<const uint2 *>(p.codes + r * (p.K / 2) + b * 8));
-    const int64_t sb = kFmt == kNv ? b : b / 2;
-    const uint32_t byte = __ldg(p.scales + scale_word(r, sb / 4, KT) + (sb & 3));
-    float s, f;
-    if (kFmt == kNv) {
-        s = from_e4m3(byte);
-        f = __ldg(p.factor + r);
-    } else {
-        // 2^(byte - 127); byte 0 is 2^-127, a subnormal, and 255 NaN
-        s = byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
-        f = 1.0f;
-    }
-    uint32_t o[8];
+    const int64_t b0 = (g - r * per_row) * (32 * kDeqPieces) + lane;
+    const float f = kFmt == kNv ? __ldg(p.factor + r) : 1.0f;
+    uint32_t c[kDeqPieces], byte[kDeqPieces];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t q[4];
-        from_e2m1x8(h == 0 ? c.x : c.y, q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&q[i]));
-            o[4 * h + i] = pack_bf16x2(v.x * s * f, v.y * s * f);
+    for (int i = 0; i < kDeqPieces; ++i) {
+        const int64_t b = b0 + i * 32;
+        c[i] = byte[i] = 0;
+        if (b < np) {
+            c[i] = __ldg(reinterpret_cast<const uint32_t *>(p.codes + r * (p.K / 2) + b * 4));
+            byte[i] = __ldg(p.scales + scale_row(r, KT) + scale_tile<kFmt>(static_cast<int>(b)) * int64_t{512} +
+                            (b / kBlockLanes<kFmt> & 3));
         }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.y + r * p.K + b * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int i = 0; i < kDeqPieces; ++i) {
+        const int64_t b = b0 + i * 32;
+        if (b >= np)
+            return;
+        float s;
+        if (kFmt == kNv)
+            s = from_e4m3(byte[i]);
+        else    // 2^(byte - 127); byte 0 is 2^-127, a subnormal, and 255 NaN
+            s = byte[i] == 255u ? __uint_as_float(0x7FC00000u)
+                                : __uint_as_float(byte[i] == 0u ? 0x00400000u : byte[i] << 23);
+        uint32_t q[4], o[4];
+        from_e2m1x8(c[i], q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&q[k]));
+            o[k] = pack_bf16x2(v.x * s * f, v.y * s * f);
+        }
+        *reinterpret_cast<uint4 *>(p.y + r * p.K + b * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 }
 
 } // namespace fp4

@@ -521,48 +521,48 @@ __device__ __forceinline__ void row_tops(S &sm, const GemmParams &p, const uint1
     }
 }
 
-// kQuant's four warps: the CTA's slices of x, coded into the stages.  Thread i takes block
-// i % 16 of 16 values of a slice, row i / 16.
+// kQuant's four warps: the CTA's slices of x, coded into the stages.  A warp takes one row,
+// a lane its 8 values of a slice.
 template <int kFmt, class S>
-__device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, const uint16_t *x, int ks0, int ks1, int tid,
+__device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, const uint16_t *x, int ks0, int ks1, int r,
                                                 uint32_t lane, volatile int *abort)
 {
-    const int64_t nb = p.K / 16;
-    const int b = tid & 15, r = tid >> 4;
+    static_assert(kQuantRows == 4, "a warp a row");
+    const int64_t np = p.K / 8;
+    const int b = static_cast<int>(lane);
     const bool mine = r < p.M;
     const uint16_t *src = x + r * p.K;
-    uint32_t w[8] = {};
-    if (mine && static_cast<int64_t>(ks0) * 16 + b < nb)
-        load16(src + (static_cast<int64_t>(ks0) * 16 + b) * 16, w);
+    uint32_t w[4] = {};
+    if (mine && static_cast<int64_t>(ks0) * 32 + b < np)
+        load8(src + (static_cast<int64_t>(ks0) * 32 + b) * 8, w);
     Row row{};
     if (kFmt == kNv) {
         uint32_t t = 0;
         for (int i = 0; i < 4; ++i)
-            t = max(t, sm.top[i][r & (kQuantRows - 1)]);
+            t = max(t, sm.top[i][r]);
         row = row_of(t);
-        if (b == 0 && r < kQuantRows)
+        if (b == 0)
             sm.factor[r] = row.factor;
     }
     uint32_t it = 0;
     for (int ks = ks0; ks < ks1; ++ks, ++it) {
         const uint32_t s = it % S::kStages, ph = (it / S::kStages) & 1;
-        const bool in = mine && static_cast<int64_t>(ks) * 16 + b < nb;
-        uint32_t m = in ? amax16(w) : 0, byte = 0;
-        if (kFmt == kMx)
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        uint2 o = make_uint2(0, 0);
+        const bool in = mine && static_cast<int64_t>(ks) * 32 + b < np;
+        const uint32_t m = block_amax<kFmt>(in ? amax8(w) : 0);
+        uint32_t byte = 0, o = 0;
         if (in)
-            o = encode16<kFmt>(w, m, row, byte);
+            o = encode8<kFmt>(w, m, row, byte);
         const uint32_t word = gather_scales<kFmt>(byte);
-        const int64_t nx = static_cast<int64_t>(ks + 1) * 16 + b;
-        if (mine && ks + 1 < ks1 && nx < nb)
-            load16(src + nx * 16, w);
+        const int64_t nx = static_cast<int64_t>(ks + 1) * 32 + b;
+        if (mine && ks + 1 < ks1 && nx < np)
+            load8(src + nx * 8, w);
         if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort))
             break;
         if (mine) {
-            *reinterpret_cast<uint2 *>(sm.x[s] + r * 128 + (((b >> 1) ^ (r & 7)) << 4) + (b & 1) * 8) = o;
+            // row r of the 128-byte-swizzled tile: 16-byte piece b / 4, XOR the row
+            *reinterpret_cast<uint32_t *>(sm.x[s] + r * 128 + (((b >> 2) ^ r) << 4) + (b & 3) * 4) = o;
             if (stores_scales<kFmt>(b))
-                *reinterpret_cast<uint32_t *>(sm.sfx[s] + (b / (kFmt == kNv ? 4 : 8)) * 512 + r * 16) = word;
+                *reinterpret_cast<uint32_t *>(sm.sfx[s] + scale_tile<kFmt>(b) * 512 + r * 16) = word;
         }
         gemm::fence_proxy_async_smem();      // the products read shared memory as the TMA does
         __syncwarp();
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
             __syncwarp();
         }
     } else if (kQuant) {
-        quantize_slices<kFmt>(sm, p, x, ks0, ks1, static_cast<int>(threadIdx.x) - 64, lane, abort);
+        quantize_slices<kFmt>(sm, p, x, ks0, ks1, warp - 2, lane, abort);
     }
     // The epilogue's thread owns output n and the tokens of this CTA's tile.
     float *part = reinterpret_cast<float *>(sm.w);

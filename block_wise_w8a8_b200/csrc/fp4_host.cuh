@@ -34,27 +34,66 @@ w8a8_status_t fp4_shape(int64_t rows, int64_t K)
 }
 
 // ------------------------------------------------------------------ quantizer
-// W warps a row, P pieces of 16 values a lane.
+// One row a CTA of W warps, P pieces of 8 values a lane.
 template <int kFmt, int W, int P>
-w8a8_status_t launch_fp4_quantize_t(const fp4::QParams &p, cudaStream_t stream)
+w8a8_status_t launch_fp4_rows(const fp4::QParams &p, cudaStream_t stream)
 {
-    constexpr int rows = fp4::kWarps / W;
-    const int64_t grid = (p.rows_pad + rows - 1) / rows;
-    fp4::quantize_kernel<kFmt, W, P><<<static_cast<unsigned>(grid), fp4::kWarps * 32, 0, stream>>>(p);
+    fp4::quantize_kernel<kFmt, W, P><<<static_cast<unsigned>(p.rows_pad), W * 32, 0, stream>>>(p);
     return launch_status();
 }
 
-template <int kFmt, int P>
-w8a8_status_t launch_fp4_quantize_p(const fp4::QParams &p, cudaStream_t stream)
+// As many CTAs as fit, each with a ring of rows.
+template <int kFmt, int W>
+w8a8_status_t launch_fp4_stream(const fp4::QParams &p, int dev, cudaStream_t stream)
 {
-    const int64_t pieces = p.K / 16;
-    if (pieces <= 32 * P)
-        return launch_fp4_quantize_t<kFmt, 1, P>(p, stream);
-    if (pieces <= 64 * P)
-        return launch_fp4_quantize_t<kFmt, 2, P>(p, stream);
-    if (pieces <= 128 * P)
-        return launch_fp4_quantize_t<kFmt, 4, P>(p, stream);
-    return launch_fp4_quantize_t<kFmt, 8, P>(p, stream);
+    constexpr int kResident = fp4::kStreamWarps / W;
+    const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(fp4::StreamTail<W>);
+    const int stages = static_cast<int>(std::min<size_t>(fp4::kMaxRing, budget / (2 * static_cast<size_t>(p.K))));
+    const size_t smem = static_cast<size_t>(stages) * 2 * p.K + sizeof(fp4::StreamTail<W>);
+    auto kern = fp4::quantize_stream_kernel<kFmt, W>;
+    constexpr int slot = kFmt * 5 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : 4);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_dev[dev].fp4_stream_attr_set[slot]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(budget + sizeof(fp4::StreamTail<W>)));
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+            g_dev[dev].fp4_stream_attr_set[slot] = true;
+        }
+    }
+    const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(g_dev[dev].sms) * kResident);
+    kern<<<static_cast<unsigned>(grid), W * 32, smem, stream>>>(p, stages);
+    return launch_status();
+}
+
+// The ring from 2 rows a resident CTA on, where a lane has up to 32 values; a row on its own
+// is split over as many warps as it fills with 8 values a lane, up to 16.
+template <int kFmt>
+w8a8_status_t launch_fp4_quantize_t(const fp4::QParams &p, int dev, cudaStream_t stream)
+{
+    const int64_t k = p.K, per_warp = 2 * g_dev[dev].sms * fp4::kStreamWarps;
+    if (k <= 1024 && p.rows >= per_warp)
+        return launch_fp4_stream<kFmt, 1>(p, dev, stream);
+    if (k > 1024 && k <= 2048 && p.rows >= per_warp / 2)
+        return launch_fp4_stream<kFmt, 2>(p, dev, stream);
+    if (k > 2048 && k <= 4096 && p.rows >= per_warp / 4)
+        return launch_fp4_stream<kFmt, 4>(p, dev, stream);
+    if (k > 4096 && k <= 8192 && p.rows >= per_warp / 8)
+        return launch_fp4_stream<kFmt, 8>(p, dev, stream);
+    if (k > 8192 && k <= 16384 && p.rows >= per_warp / 16)
+        return launch_fp4_stream<kFmt, 16>(p, dev, stream);
+    if (k <= 256)
+        return launch_fp4_rows<kFmt, 1, 1>(p, stream);
+    if (k <= 512)
+        return launch_fp4_rows<kFmt, 2, 1>(p, stream);
+    if (k <= 1024)
+        return launch_fp4_rows<kFmt, 4, 1>(p, stream);
+    if (k <= 2048)
+        return launch_fp4_rows<kFmt, 8, 1>(p, stream);
+    if (k <= 4096)
+        return launch_fp4_rows<kFmt, 16, 1>(p, stream);
+    return launch_fp4_rows<kFmt, 16, 4>(p, stream);
 }
 
 w8a8_status_t launch_fp4_quantize(const uint16_t *x, int64_t rows, int64_t K, int format, uint8_t *codes,
@@ -70,10 +109,8 @@ w8a8_status_t launch_fp4_quantize(const uint16_t *x, int64_t rows, int64_t K, in
     p.codes = codes;
     p.scales = scales;
     p.factor = factor;
-    const bool spread = rows < 8 * g_dev[dev].sms && K <= 16 * 32 * fp4::kWarps;
-    if (format == W8A8_FP4_MX)
-        return spread ? launch_fp4_quantize_p<fp4::kMx, 1>(p, stream) : launch_fp4_quantize_p<fp4::kMx, 4>(p, stream);
-    return spread ? launch_fp4_quantize_p<fp4::kNv, 1>(p, stream) : launch_fp4_quantize_p<fp4::kNv, 4>(p, stream);
+    return format == W8A8_FP4_MX ? launch_fp4_quantize_t<fp4::kMx>(p, dev, stream)
+                                 : launch_fp4_quantize_t<fp4::kNv>(p, dev, stream);
 }
 
 // ------------------------------------------------------------------ product
@@ -273,36 +310,75 @@ w8a8_status_t check_fp4_weight(const w8a8_fp4_weight_t *w, int64_t K)
 }
 
 // ------------------------------------------------------------------ block norm
-template <int kOut, int V, int W, int P, bool kLong>
-w8a8_status_t launch_block_norm_t(const bnorm::Params &p, cudaStream_t stream)
+template <int kOut, int W, int P, bool kLong>
+w8a8_status_t launch_norm_rows(const bnorm::Params &p, cudaStream_t stream)
 {
-    constexpr int rows = bnorm::kWarps / W;
-    const int64_t total = kOut == bnorm::kOutBf16 ? p.M : p.M_pad;
-    const int64_t grid = (total + rows - 1) / rows;
-    bnorm::block_norm_kernel<kOut, V, W, P, kLong>
-        <<<static_cast<unsigned>(grid), bnorm::kWarps * 32, 0, stream>>>(p);
+    const int64_t grid = kOut == bnorm::kOutBf16 ? p.M : p.M_pad;
+    bnorm::row_kernel<kOut, W, P, kLong><<<static_cast<unsigned>(grid), W * 32, 0, stream>>>(p);
     return launch_status();
 }
 
-// The fewest warps that hold a row with one piece of 16 values a lane, then more pieces.
-template <int kOut, int V>
-w8a8_status_t launch_block_norm_v(const bnorm::Params &p, cudaStream_t stream)
+// As many CTAs as fit, each with a ring of `stages` rows.
+template <int kOut, int W, int P>
+w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
 {
-    constexpr int Q = 16 / V;
-    const int64_t k = p.K;
+    constexpr int kResident = P > 2 ? 1 : bnorm::kStreamWarps / W;    // CTAs a SM
+    const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(bnorm::StreamTail<W>);
+    p.stages = static_cast<int32_t>(std::min<size_t>(fp4::kMaxRing, budget / (4 * static_cast<size_t>(p.K))));
+    const size_t smem = static_cast<size_t>(p.stages) * 4 * p.K + sizeof(bnorm::StreamTail<W>);
+    auto kern = bnorm::stream_kernel<kOut, W, P>;
+    constexpr int slot = (kOut + 1) * 6 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : P == 2 ? 4 : 5);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_dev[dev].norm_stream_attr_set[slot]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(budget + sizeof(bnorm::StreamTail<W>)));
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+            g_dev[dev].norm_stream_attr_set[slot] = true;
+        }
+    }
+    const int64_t grid = std::min<int64_t>(p.M, static_cast<int64_t>(g_dev[dev].sms) * kResident);
+    kern<<<static_cast<unsigned>(grid), W * 32, smem, stream>>>(p);
+    return launch_status();
+}
+
+// The ring from 4 rows a resident CTA on.  There a lane has 16 values (32 in the longest
+// rows), which spreads a row's reductions over enough of them; a row on its own is split
+// over as many warps as it fills.
+template <int kOut>
+w8a8_status_t launch_block_norm(const bnorm::Params &p, cudaStream_t stream)
+{
+    int dev;
+    W8A8_TRY(current_device(dev));
+    const int64_t k = p.K, per_warp = 4 * g_dev[dev].sms * bnorm::kStreamWarps;
+    if (k <= 512 && p.M >= per_warp)
+        return launch_norm_stream<kOut, 1, 2>(p, dev, stream);
+    if (k > 512 && k <= 1024 && p.M >= per_warp / 2)
+        return launch_norm_stream<kOut, 2, 2>(p, dev, stream);
+    if (k > 1024 && k <= 2048 && p.M >= per_warp / 4)
+        return launch_norm_stream<kOut, 4, 2>(p, dev, stream);
+    if (k > 2048 && k <= 4096 && p.M >= per_warp / 8)
+        return launch_norm_stream<kOut, 8, 2>(p, dev, stream);
+    if (k > 4096 && k <= 8192 && p.M >= per_warp / 16)
+        return launch_norm_stream<kOut, 16, 2>(p, dev, stream);
+    if (k > 8192 && k <= 16384 && p.M >= per_warp / 16)
+        return launch_norm_stream<kOut, 16, 4>(p, dev, stream);
+    if (k <= 256)
+        return launch_norm_rows<kOut, 1, 1, false>(p, stream);
     if (k <= 512)
-        return launch_block_norm_t<kOut, V, 1, Q, false>(p, stream);
+        return launch_norm_rows<kOut, 2, 1, false>(p, stream);
     if (k <= 1024)
-        return launch_block_norm_t<kOut, V, 2, Q, false>(p, stream);
+        return launch_norm_rows<kOut, 4, 1, false>(p, stream);
     if (k <= 2048)
-        return launch_block_norm_t<kOut, V, 4, Q, false>(p, stream);
+        return launch_norm_rows<kOut, 8, 1, false>(p, stream);
     if (k <= 4096)
-        return launch_block_norm_t<kOut, V, 8, Q, false>(p, stream);
+        return launch_norm_rows<kOut, 16, 1, false>(p, stream);
     if (k <= 8192)
-        return launch_block_norm_t<kOut, V, 8, 2 * Q, false>(p, stream);
+        return launch_norm_rows<kOut, 16, 2, false>(p, stream);
     if (k <= 16384)
-        return launch_block_norm_t<kOut, V, 8, 4 * Q, false>(p, stream);
-    return launch_block_norm_t<kOut, V, 8, 2 * Q, true>(p, stream);
+        return launch_norm_rows<kOut, 16, 4, false>(p, stream);
+    return launch_norm_rows<kOut, 16, 2, true>(p, stream);
 }
 
 // Arguments that both forms share -> p.

@@ -36,6 +36,8 @@ struct DeviceInfo {
     bool norm_attr_set[4] = {false, false, false, false};
     int norm_max_clusters[norm::kMaxCluster + 1] = {};    // by cluster size, 0 = unknown
     int fp4_pairs[4] = {};                                 // by format and store: pairs that fit, 0 = unknown
+    bool norm_stream_attr_set[18] = {};                    // bnorm::stream_kernel by output, warps and pieces
+    bool fp4_stream_attr_set[10] = {};                     // fp4::quantize_stream_kernel by format and warps
     bool fp4_skinny_attr_set[10] = {};                     // by format and token tile, quantizing or not
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -1059,7 +1061,8 @@ w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, c
     if (!aligned16(y))
         return W8A8_ERR_ALIGNMENT;
     const fp4::DParams p{codes, scales, factor, rows, K, y};
-    const int64_t grid = (rows * ((K / 16 + 31) / 32) + fp4::kWarps - 1) / fp4::kWarps;
+    const int64_t run = 256 * fp4::kDeqPieces;
+    const int64_t grid = (rows * ((K + run - 1) / run) + fp4::kWarps - 1) / fp4::kWarps;
     if (grid > 0x7FFFFFFF)
         return W8A8_ERR_SHAPE;
     auto kern = format == W8A8_FP4_MX ? fp4::dequantize_kernel<fp4::kMx> : fp4::dequantize_kernel<fp4::kNv>;
@@ -1166,10 +1169,7 @@ w8a8_status_t w8a8_block_norm(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int po
     if (!aligned16(n_out))
         return W8A8_ERR_ALIGNMENT;
     p.n_out = n_out;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // 16 values a lane wherever 4-bit output exists too, so that both forms add a row's
-    // squares in the same order and give the same bits
-    return K % 32 == 0 ? launch_block_norm_v<bnorm::kOutBf16, 16>(p, st) : launch_block_norm_v<bnorm::kOutBf16, 8>(p, st);
+    return launch_block_norm<bnorm::kOutBf16>(p, static_cast<cudaStream_t>(stream));
 }
 
 w8a8_status_t w8a8_block_norm_fp4(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,
@@ -1193,7 +1193,7 @@ w8a8_status_t w8a8_block_norm_fp4(const w8a8_bf16_t *h, const w8a8_bf16_t *y, in
     p.scales = scales;
     p.factor = factor;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return format == W8A8_FP4_MX ? launch_block_norm_v<fp4::kMx, 16>(p, st) : launch_block_norm_v<fp4::kNv, 16>(p, st);
+    return format == W8A8_FP4_MX ? launch_block_norm<fp4::kMx>(p, st) : launch_block_norm<fp4::kNv>(p, st);
 }
 
 w8a8_status_t w8a8_debug_block_sums(const int8_t *xq, const int8_t *wq, int64_t M, int64_t K,

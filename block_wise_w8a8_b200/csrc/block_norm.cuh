@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
         // every thread has read the slot
         if (threadIdx.x == 0 && r + static_cast<int64_t>(S) * gridDim.x < p.M)
             fetch(r + static_cast<int64_t>(S) * gridDim.x, s);
-        uint32_t top = 0;
+        uint32_t top = 0, m[P] = {};
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int b = b0 + i * kStep;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
                 if constexpr (kOut == kOutBf16)
                     *reinterpret_cast<uint4 *>(p.n_out + r * p.K + b * 8) = pack4(h[i]);
                 else
-                    top = max(top, fp4::amax8(h[i]));
+                    top = max(top, m[i] = fp4::amax8(h[i]));
             }
         }
         if constexpr (kOut != kOutBf16) {
@@ -281,13 +281,13 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             if (kOut == fp4::kNv) {
                 row = fp4::row_of(fp4::row_top<W>(top, sm.top[par], warp, lane));
                 if (threadIdx.x == 0)
-                    p.factor[r] = row.factor;
+                    p.factor[r] = row.factor();
             }
             uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + fp4::scale_row(r, KT);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int b = b0 + i * kStep;
-                fp4::store_piece<kOut>(codes, scales, b, b < np, fp4::pieces_padded<kOut>(KT), row, h[i]);
+                fp4::store_piece<kOut>(codes, scales, b, b < np, fp4::pieces_padded<kOut>(KT), row, h[i], m[i]);
             }
         }
         if (++s == S) {
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
     rstd = rstd_of(row_sum<W>(acc.x + acc.y, s_red[1], warp, lane), inv_k, p.eps);
 
     // n, and for kNv its largest magnitude; a long row's n is formed again for its codes
-    uint32_t top = 0;
+    uint32_t top = 0, m[P] = {};
     for (int at_c = 0; at_c < (kLong && kOut == fp4::kMx ? 0 : np); at_c += kChunk) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
                 if constexpr (kOut == kOutBf16)
                     *reinterpret_cast<uint4 *>(p.n_out + at + static_cast<size_t>(b) * 8) = pack4(h[i]);
                 else
-                    top = max(top, fp4::amax8(h[i]));
+                    top = max(top, m[i] = fp4::amax8(h[i]));
             }
         }
     }
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
         if (kOut == fp4::kNv) {
             row = fp4::row_of(fp4::row_top<W>(top, s_top, warp, lane));
             if (threadIdx.x == 0)
-                p.factor[r] = row.factor;
+                p.factor[r] = row.factor();
         }
         const int64_t KT = fp4::scale_tiles(p.K, kOut);
         const int np_pad = fp4::pieces_padded<kOut>(KT);
@@ -416,8 +416,9 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
                     unpack4(*reinterpret_cast<const uint4 *>(p.h_out + at + static_cast<size_t>(b) * 8), y[i]);
                     load_pre(p, int64_t{8} * b, mod, pre[0]);
                     normalise(pre[0], rstd, y[i], h[i]);
+                    m[i] = fp4::amax8(h[i]);
                 }
-                fp4::store_piece<kOut>(codes, scales, b, b < np, np_pad, row, h[i]);
+                fp4::store_piece<kOut>(codes, scales, b, b < np, np_pad, row, h[i], m[i]);
             }
         }
     }

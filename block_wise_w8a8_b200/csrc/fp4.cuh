@@ -23,9 +23,11 @@
 //        boundary of E4M3 is j 2^i with odd j < 32, of E2M1 with odd j <= 7, so a quotient
 //        off the boundary is off by 2^-13 (scale) or 2^-14.9 (code) of itself at least: two
 //        different whole numbers, the larger below 32 * 2^8 or 7 * 2^12, differ by one.  The
-//        products with reciprocals below are within 2^-21 of the quotients (four roundings
-//        and a reciprocal good to one unit in the last place).  Rounded to 17 significant bits they
-//        lie on a boundary only if the quotient does, and on the same side of it otherwise.
+//        products with reciprocals below are within 2^-21 of the quotients (three roundings
+//        and two reciprocals good to one unit in the last place).  Rounded to 17 significant
+//        bits (scale), or to a multiple of 2^-17 (code: at most 8, boundaries from 0.25 up),
+//        they lie on a boundary only if the quotient does, and on the same side otherwise.
+//        (A negative value below 2^-18 of the unit becomes +0 on the way, others -0.)
 //
 // Scales lie as tcgen05 block-scaled products read them: 512-byte tiles of 128 rows x 4
 // scales along K, tile [row / 128][block / 4], byte 16 (row % 32) + 4 (row % 128 / 32) +
@@ -122,24 +124,29 @@ __device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[4])
 // What a row's factor and its blocks' scales are taken from (kNv), given the row's largest
 // magnitude pattern.
 struct Row {
-    float to_scale;   // 448 / A; unused for kMx, like the rest
+    float top;        // A; unused for kMx, like the rest
+    float to_scale;   // 448 / A
     float to_code;    // 2688 / A
-    float factor;     // what is stored
     bool bad;         // the row holds an infinity or a NaN
+    __device__ __forceinline__ float factor() const      // what is stored
+    {
+        return bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(top, kRowDiv);
+    }
 };
 __device__ __forceinline__ Row row_of(uint32_t amax_bits)
 {
     Row r;
     r.bad = amax_bits >= 0x7F80u;
-    const float top = r.bad ? 1.0f : fmaxf(__uint_as_float(amax_bits << 16), kTiny);
-    r.factor = r.bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(top, kRowDiv);
-    r.to_scale = __fdiv_rn(448.0f, top);
-    r.to_code = __fdiv_rn(kRowDiv, top);
+    r.top = r.bad ? 1.0f : fmaxf(__uint_as_float(amax_bits << 16), kTiny);
+    const float q = reciprocal(r.top * (1.0f / 4096.0f));       // 4096 / A, a normal number
+    r.to_scale = 0.109375f * q;
+    r.to_code = 0.65625f * q;
     return r;
 }
 
-// A lane holds 8 consecutive values (so that a warp's loads and stores are 512 contiguous
-// bytes); 2 (kNv) or 4 (kMx) neighbouring lanes share a block.  Lane order = order along K.
+// Where a lane holds 8 consecutive values (a warp's loads and stores of BF16 are then 512
+// contiguous bytes), 2 (kNv) or 4 (kMx) neighbouring lanes share a block.  Lane order =
+// order along K.
 template <int kFmt>
 constexpr int kBlockLanes = kFmt == kMx ? 4 : 2;
 
@@ -151,68 +158,86 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t m)
     return kFmt == kMx ? max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) : m;
 }
 
-// Codes of 8 values (4 packed BF16 pairs) and the scale byte of their block, given the
-// block's largest magnitude pattern.
-template <int kFmt>
-__device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], uint32_t m, const Row &row, uint32_t &byte)
-{
+// The scale byte of a block, given its largest magnitude pattern m, and what its values are
+// multiplied by before they are rounded to E2M1; codes are 0 where `zero`.
+struct Unit {
+    uint32_t byte;
     float mult;
     bool zero;
+};
+template <int kFmt>
+__device__ __forceinline__ Unit unit_of(uint32_t m, const Row &row)
+{
+    Unit u;
     if (kFmt == kMx) {
         const uint32_t e = m >> 7;                       // exponent field of the largest
-        zero = e == 255u;
-        byte = zero ? 255u : (e > 2u ? e - 2u : 0u);
-        mult = zero ? 0.0f : __uint_as_float((254u - byte) << 23);
+        u.zero = e == 255u;
+        u.byte = u.zero ? 255u : (e > 2u ? e - 2u : 0u);
+        u.mult = u.zero ? 0.0f : __uint_as_float((254u - u.byte) << 23);
     } else {
-        zero = row.bad;
-        byte = zero ? 0u : to_e4m3(round17(__uint_as_float(m << 16) * row.to_scale));
-        mult = byte == 0u ? 0.0f : row.to_code * reciprocal(from_e4m3(byte));
+        u.zero = row.bad;
+        u.byte = u.zero ? 0u : to_e4m3(round17(__uint_as_float(m << 16) * row.to_scale));
+        u.mult = u.byte == 0u ? 0.0f : row.to_code * reciprocal(from_e4m3(u.byte));
     }
+    return u;
+}
+
+// Codes of 8 values (4 packed BF16 pairs).
+template <int kFmt>
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const Unit &u)
+{
     float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 q = __fmul2_rn(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), make_float2(mult, mult));
-        v[2 * i] = kFmt == kNv ? round17(q.x) : q.x;
-        v[2 * i + 1] = kFmt == kNv ? round17(q.y) : q.y;
+        const float2 x = make_float2(bf16_lo(w[i]), bf16_hi(w[i])), m2 = make_float2(u.mult, u.mult);
+        float2 q;
+        if (kFmt == kMx) {
+            q = __fmul2_rn(x, m2);
+        } else {                 // to a multiple of 2^-17: FP32's step between 64 and 128
+            q = __ffma2_rn(x, m2, make_float2(96.0f, 96.0f));
+            q = __fadd2_rn(q, make_float2(-96.0f, -96.0f));
+        }
+        v[2 * i] = q.x;
+        v[2 * i + 1] = q.y;
     }
-    return zero ? 0u : e2m1x8(v);
+    return u.zero ? 0u : e2m1x8(v);
+}
+template <int kFmt>
+__device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[4], uint32_t m, const Row &row, uint32_t &byte)
+{
+    const Unit u = unit_of<kFmt>(m, row);
+    byte = u.byte;
+    return codes8<kFmt>(w, u);
 }
 
-// Scale bytes, one a block's lanes -> the four scales of a tile's row in one word, on the
-// lane that stores it: every eighth (kNv) or sixteenth (kMx).
+// Offset of the scale of piece b's block from its row's first, and whether this lane stores
+// it.  A byte each: gathering a tile's four into a word first takes two shuffles and more
+// instructions than the stores it saves.
 template <int kFmt>
-__device__ __forceinline__ uint32_t gather_scales(uint32_t byte)
+__device__ __forceinline__ uint32_t scale_offset(int b)
 {
-    constexpr uint32_t kFull = 0xFFFFFFFFu;
-    constexpr int step = kBlockLanes<kFmt>;
-    uint32_t v = byte | (__shfl_down_sync(kFull, byte, step) << 8);
-    return v | (__shfl_down_sync(kFull, v, 2 * step) << 16);
-}
-// Whether piece b of 8 values is the first of a scale word, and which tile along K it is in.
-template <int kFmt>
-__device__ __forceinline__ bool stores_scales(int b)
-{
-    return (b & (4 * kBlockLanes<kFmt> - 1)) == 0;
+    constexpr int lanes = kBlockLanes<kFmt>;
+    return static_cast<uint32_t>(b / (4 * lanes)) * 512 + (b / lanes & 3);
 }
 template <int kFmt>
-__device__ __forceinline__ int scale_tile(int b)
+__device__ __forceinline__ bool stores_scale(int b)
 {
-    return b / (4 * kBlockLanes<kFmt>);
+    return (b & (kBlockLanes<kFmt> - 1)) == 0;
 }
 
-// Codes of a lane's piece b (of np) of a row, and the scales of the 4 blocks around it; every
-// lane of the warp takes part, `in` (b < np) or not.  codes and scales: the row's.
+// Codes and block scale of a lane's piece b of a row, from its values and their largest
+// magnitude m; every lane of the warp takes part, `in` (b < np) or not.  codes and scales:
+// the row's.
 template <int kFmt>
 __device__ __forceinline__ void store_piece(uint8_t *codes, uint8_t *scales, int b, bool in, int np_pad, const Row &row,
-                                            const uint32_t (&w)[4])
+                                            const uint32_t (&w)[4], uint32_t m)
 {
-    const uint32_t m = block_amax<kFmt>(in ? amax8(w) : 0);
+    m = block_amax<kFmt>(in ? m : 0);
     uint32_t byte = 0;
     if (in)
         *reinterpret_cast<uint32_t *>(codes + static_cast<uint32_t>(b) * 4) = encode8<kFmt>(w, m, row, byte);
-    const uint32_t word = gather_scales<kFmt>(byte);
-    if (stores_scales<kFmt>(b) && b < np_pad)
-        *reinterpret_cast<uint32_t *>(scales + static_cast<size_t>(scale_tile<kFmt>(b)) * 512) = word;
+    if (stores_scale<kFmt>(b) && b < np_pad)
+        scales[scale_offset<kFmt>(b)] = static_cast<uint8_t>(byte);
 }
 // Pieces of 8 values of a row with its last scale tile filled up.
 template <int kFmt>
@@ -283,7 +308,7 @@ __global__ void __launch_bounds__(W * 32) quantize_kernel(const QParams p)
     const int b0 = warp * 32 + static_cast<int>(lane);
     constexpr int kStep = W * 32;
     const uint16_t *xr = p.x + r * p.K;
-    uint32_t w[P][4];
+    uint32_t w[P][4], m[P];
     uint32_t top = 0;
     const bool once = np <= kStep * P;
     if (kFmt == kNv || once) {
@@ -294,24 +319,28 @@ __global__ void __launch_bounds__(W * 32) quantize_kernel(const QParams p)
                     load8(xr + static_cast<size_t>(b0 + c + i * kStep) * 8, w[i]);
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (kFmt == kNv && b0 + c + i * kStep < np)
-                    top = max(top, amax8(w[i]));
+                if (b0 + c + i * kStep < np) {
+                    m[i] = amax8(w[i]);
+                    top = max(top, m[i]);
+                }
         }
     }
     Row row{};
     if (kFmt == kNv) {
         row = row_of(row_top<W>(top, s_top, warp, lane));
         if (threadIdx.x == 0)
-            p.factor[r] = row.factor;
+            p.factor[r] = row.factor();
     }
     uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
     for (int c = 0; c < np_pad; c += kStep * P) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int b = b0 + c + i * kStep;
-            if (!once && b < np)
+            if (!once && b < np) {
                 load8(xr + static_cast<size_t>(b) * 8, w[i]);
-            store_piece<kFmt>(codes, scales, b, b < np, np_pad, row, w[i]);
+                m[i] = amax8(w[i]);
+            }
+            store_piece<kFmt>(codes, scales, b, b < np, np_pad, row, w[i], m[i]);
         }
     }
 }
@@ -328,8 +357,10 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // Many rows.  CTAs of W warps stay, take every gridDim.x-th row, and have the next rows copied
 // into a ring in shared memory (a bulk copy each) while they code: with a CTA a row the loads,
 // the arithmetic and the stores of the few CTAs that fit a SM hardly overlap (16384 x 4096
-// nvfp4: 49 us).  A lane has up to 4 pieces of 8 values, K <= 1024 W.
-constexpr int kStreamPieces = 4;
+// nvfp4: 49 us).  Then the instructions bound it (ncu: 72% of the issue slots at 15 a value),
+// so a lane takes 16 consecutive values, a whole block (kNv) or half of one: what a block costs
+// is paid half as often as with 8.  Up to kStreamPieces of them, K <= 1024 W.
+constexpr int kStreamPieces = 2;
 constexpr int kStreamWarps = 32;                 // warps a SM
 constexpr int kMaxRing = 16;                     // rows of a ring at most
 template <int W>
@@ -349,11 +380,17 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
-    const int np = static_cast<int>(p.K / 8);
+    const int np = static_cast<int>(p.K / 16);
     const int64_t KT = scale_tiles(p.K, kFmt);
-    const int np_pad = pieces_padded<kFmt>(KT);
+    constexpr int kTileBlocks = kFmt == kMx ? 8 : 4;         // pieces of 16 a scale tile
+    const int np_pad = static_cast<int>(KT) * kTileBlocks;
     const int b0 = warp * 32 + static_cast<int>(lane);
     constexpr int kStep = W * 32;
+    const bool stores = kFmt == kNv || (lane & 1) == 0;
+    const uint32_t scale_at = static_cast<uint32_t>(b0 / kTileBlocks) * 512 + (kFmt == kNv ? b0 & 3 : b0 / 2 & 3);
+    // the order in which a lane reads its two 16-byte halves: 8 neighbouring lanes then cover
+    // all of the shared memory's banks
+    const uint32_t first = lane >> 2 & 1;
     volatile int *abort = &sm.abort;
 
     auto fetch = [&](int64_t r, int s) {
@@ -377,24 +414,30 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
         // reaches every barrier.
         mbar_wait(&sm.full[s], phase, abort);
         const uint8_t *slot = ring + static_cast<size_t>(s) * row_bytes;
-        uint32_t w[P][4];
+        uint32_t w[P][2][4], m[P];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+            m[i] = 0;
             if (b0 + i * kStep < np) {
-                const uint4 v = ld_shared_v4(slot + (b0 + i * kStep) * 16);
-                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    const uint4 v = ld_shared_v4(slot + (b0 + i * kStep) * 32 + ((first ^ h) << 4));
+                    w[i][h][0] = v.x; w[i][h][1] = v.y; w[i][h][2] = v.z; w[i][h][3] = v.w;
+                }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (b0 + i * kStep < np)
+                m[i] = max(amax8(w[i][0]), amax8(w[i][1]));
+            top = max(top, m[i]);
         }
         Row row{};
         if (kFmt == kNv) {
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                top = max(top, amax8(w[i]));
             row = row_of(row_top<W>(top, sm.top[par], warp, lane));
             if (threadIdx.x == 0)
-                p.factor[r] = row.factor;
+                p.factor[r] = row.factor();
         } else if (W > 1) {
             __syncthreads();
         }
@@ -405,9 +448,20 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
             fetch(r + static_cast<int64_t>(stages) * gridDim.x, s);
         uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i * kStep < np_pad)
-                store_piece<kFmt>(codes, scales, b0 + i * kStep, b0 + i * kStep < np, np_pad, row, w[i]);
+        for (int i = 0; i < P; ++i) {
+            const int b = b0 + i * kStep;
+            if (kFmt == kMx)
+                m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
+            Unit u{};
+            if (b < np) {
+                u = unit_of<kFmt>(m[i], row);
+                const uint32_t c0 = codes8<kFmt>(w[i][0], u), c1 = codes8<kFmt>(w[i][1], u);
+                *reinterpret_cast<uint2 *>(codes + static_cast<uint32_t>(b) * 8) =
+                    first == 0 ? make_uint2(c0, c1) : make_uint2(c1, c0);
+            }
+            if (stores && b < np_pad)
+                scales[scale_at + i * (kStep / kTileBlocks * 512)] = static_cast<uint8_t>(u.byte);
+        }
         if (++s == stages) {
             s = 0;
             phase ^= 1;
@@ -448,8 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32) dequantize_kernel(const DParams p
         c[i] = byte[i] = 0;
         if (b < np) {
             c[i] = __ldg(reinterpret_cast<const uint32_t *>(p.codes + r * (p.K / 2) + b * 4));
-            byte[i] = __ldg(p.scales + scale_row(r, KT) + scale_tile<kFmt>(static_cast<int>(b)) * int64_t{512} +
-                            (b / kBlockLanes<kFmt> & 3));
+            byte[i] = __ldg(p.scales + scale_row(r, KT) + scale_offset<kFmt>(static_cast<int>(b)));
         }
     }
 #pragma unroll

@@ -542,7 +542,7 @@ __device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, cons
             t = max(t, sm.top[i][r]);
         row = row_of(t);
         if (b == 0)
-            sm.factor[r] = row.factor;
+            sm.factor[r] = row.factor();
     }
     uint32_t it = 0;
     for (int ks = ks0; ks < ks1; ++ks, ++it) {
@@ -552,7 +552,6 @@ __device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, cons
         uint32_t byte = 0, o = 0;
         if (in)
             o = encode8<kFmt>(w, m, row, byte);
-        const uint32_t word = gather_scales<kFmt>(byte);
         const int64_t nx = static_cast<int64_t>(ks + 1) * 32 + b;
         if (mine && ks + 1 < ks1 && nx < np)
             load8(src + nx * 8, w);
@@ -561,8 +560,8 @@ __device__ __forceinline__ void quantize_slices(S &sm, const GemmParams &p, cons
         if (mine) {
             // row r of the 128-byte-swizzled tile: 16-byte piece b / 4, XOR the row
             *reinterpret_cast<uint32_t *>(sm.x[s] + r * 128 + (((b >> 2) ^ r) << 4) + (b & 3) * 4) = o;
-            if (stores_scales<kFmt>(b))
-                *reinterpret_cast<uint32_t *>(sm.sfx[s] + scale_tile<kFmt>(b) * 512 + r * 16) = word;
+            if (stores_scale<kFmt>(b))
+                sm.sfx[s][r * 16 + scale_offset<kFmt>(b)] = static_cast<uint8_t>(byte);
         }
         gemm::fence_proxy_async_smem();      // the products read shared memory as the TMA does
         __syncwarp();

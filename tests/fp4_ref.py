@@ -65,6 +65,12 @@ def quantize(x, fmt):
     return torch.where(dead, 0, code).view(M, K), scales, factor
 
 
+def no_minus_zero(codes):
+    """Packed codes with every -0 (8) as 0: nvfp4 leaves a zero's sign open."""
+    low, high = codes & 15, codes >> 4
+    return torch.where(low == 8, 0, low) | (torch.where(high == 8, 0, high) << 4)
+
+
 def pack(code):
     return code[:, 0::2] | (code[:, 1::2] << 4)
 

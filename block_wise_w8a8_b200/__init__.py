@@ -513,6 +513,13 @@ def _fits(t, shape, dtype, device):
             and t.is_contiguous())
 
 
+def _bf16_out(out, like, shape, device):
+    """_out for a BF16 output; a new one is made from a tensor at hand, which takes less time."""
+    if out is None:
+        return like.new_empty(shape, dtype=torch.bfloat16)
+    return _out(out, shape, torch.bfloat16, device, "out")
+
+
 def _column(t, shape, device, name):
     """An optional BF16 input: checked, as its address (None where there is none)."""
     if t is None:
@@ -534,17 +541,21 @@ class FP4Tensor:
         fmt = _fp4_format(format)
         _need(codes, torch.uint8, "codes")
         rows, half = codes.shape
+        dev, tiles = codes.device, _fp4_tiles(rows, 2 * half, format)
         _fp4_k(2 * half)
-        self.rows, self.K, self.format, self.device = rows, 2 * half, format, codes.device
-        if not _fits(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device):
-            _in(scales, _fp4_tiles(rows, 2 * half, format), torch.uint8, codes.device, "scales")
+        self.rows, self.K, self.format, self.device = rows, 2 * half, format, dev
+        if not _fits(scales, tiles, torch.uint8, dev):
+            _in(scales, tiles, torch.uint8, dev, "scales")
         if fmt:
-            if not _fits(factor, (rows,), torch.float32, codes.device):
-                _in(factor, (rows,), torch.float32, codes.device, "factor")
+            if not _fits(factor, (rows,), torch.float32, dev):
+                _in(factor, (rows,), torch.float32, dev, "factor")
         elif factor is not None:
             raise ValueError("mxfp4 has no row factors")
         self._buffer, self._parts = None, (codes, scales, factor)
         self._ptrs = (codes.data_ptr(), scales.data_ptr(), factor.data_ptr() if fmt else None)
+
+    def _any(self):
+        return self._buffer if self._parts is None else self._parts[0]
 
     def _views(self):
         if self._parts is None:
@@ -634,7 +645,7 @@ def fp4_dequantize(q, out=None):
     """The values an FP4Tensor's codes stand for, BF16 [rows, K]."""
     if not isinstance(q, FP4Tensor):
         raise TypeError("q must be an FP4Tensor")
-    y = _out(out, (q.rows, q.K), torch.bfloat16, q.device, "out")
+    y = _bf16_out(out, q._any(), (q.rows, q.K), q.device)
     _check("w8a8_fp4_dequantize", lib().w8a8_fp4_dequantize(
         *q._ptrs, q.rows, q.K, FP4_FORMATS[q.format], y.data_ptr(), _stream(q.device)))
     return y
@@ -693,7 +704,7 @@ def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False
     _fp4_weight_on(weight, K, dev)
     b = _column(bias, (weight.N,), dev, "bias")
     shape = (*x.shape[:-1], weight.N)
-    out = x.new_empty(shape) if out is None else _out(out, shape, torch.bfloat16, dev, "out")
+    out = _bf16_out(out, x, shape, dev)
     if workspace is None:
         size = int(lib().w8a8_fp4_linear_workspace_bytes(M, K, FP4_FORMATS[weight.format]))
         if size:
@@ -716,7 +727,7 @@ def fp4_linear_prequant(q, weight, bias=None, out=None):
     if weight.format != q.format:
         raise ValueError(f"weight is {weight.format}, the activations {q.format}")
     b = _column(bias, (weight.N,), q.device, "bias")
-    out = _out(out, (q.rows, weight.N), torch.bfloat16, q.device, "out")
+    out = _bf16_out(out, q._any(), (q.rows, weight.N), q.device)
     _check("w8a8_fp4_linear_prequant", lib().w8a8_fp4_linear_prequant(
         *q._ptrs, q.rows, q.K, weight._rec, b, out.data_ptr(), _stream(q.device)))
     return out

@@ -114,6 +114,8 @@ w8a8_status_t launch_fp4_quantize(const uint16_t *x, int64_t rows, int64_t K, in
 }
 
 // ------------------------------------------------------------------ product
+// Products are launched as programmatic dependents: their set-up overlaps the end of whatever
+// precedes them on the stream, and they read nothing before that has completed.
 w8a8_status_t fp4_maps(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int format,
                        uint32_t box_rows, CUtensorMap &mc, CUtensorMap &ms)
 {
@@ -131,13 +133,13 @@ struct Fp4Operand {
 };
 
 template <int kFmt, bool kTma>
-w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream, bool pdl)
+w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::GemmParams p, cudaStream_t stream)
 {
     int dev;
     W8A8_TRY(current_device(dev));
     CUtensorMap mx, mxs, mw, mws, my;
     W8A8_TRY(fp4_maps(x.codes, x.scales, p.M, p.K, kFmt, 128, mx, mxs));
-    W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 128, mw, mws));
+    W8A8_TRY(fp4_maps(w.codes, w.scales, p.N, p.K, kFmt, 64, mw, mws));
     my = mx;
     if (kTma)
         W8A8_TRY(make_map(my, p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.M, p.N, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B));
@@ -180,8 +182,14 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
         }
         pairs = known;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, p.num_tm * p.num_tn)));
-    cfg.numAttrs = pdl ? 2 : 1;
+    const int tiles = p.num_tm * p.num_tn, tail = tiles % pairs;
+    p.num_full = p.num_units = tiles;
+    if (kTma && tail > 0 && 2 * tail <= pairs) {
+        p.num_full = tiles - tail;
+        p.num_units = tiles + tail;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, p.num_units)));
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, my, p);
     return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
@@ -189,7 +197,7 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
 // xb: BF16 activations to quantize on the way (kQuant), else null.
 template <int kFmt, int BT, bool kQuant>
 w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const Fp4Operand &w, fp4::GemmParams p,
-                                cudaStream_t stream, bool pdl)
+                                cudaStream_t stream)
 {
     int dev;
     W8A8_TRY(current_device(dev));
@@ -236,30 +244,29 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.numAttrs = kQuant ? 1 : 2;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, xb, p);
     return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
 template <int kFmt>
-w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const fp4::GemmParams &p, cudaStream_t stream,
-                                bool pdl)
+w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const fp4::GemmParams &p, cudaStream_t stream)
 {
     if (p.M <= 16)
-        return launch_fp4_skinny<kFmt, 16, false>(x, nullptr, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 16, false>(x, nullptr, w, p, stream);
     if (p.M <= 32)
-        return launch_fp4_skinny<kFmt, 32, false>(x, nullptr, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 32, false>(x, nullptr, w, p, stream);
     if (p.M <= 64)
-        return launch_fp4_skinny<kFmt, 64, false>(x, nullptr, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 64, false>(x, nullptr, w, p, stream);
     // From 65 tokens on the pair kernel is the faster one where its tiles fill enough of the
     // device: 128 x 4096 x 16384 15.2 us for 18.3, 128 x 2048 x 8192 10.5 for 13.3; but
     // 128 x 4096 x 4096, 16 tiles that it does not split along K, 12.3 for 11.5 and
     // 128 x 16384 x 4096 27.4 for 18.9.
     if (p.M <= 128 && p.N <= 4096)
-        return launch_fp4_skinny<kFmt, 128, false>(x, nullptr, w, p, stream, pdl);
-    return p.N % 8 == 0 && aligned16(p.y) ? launch_fp4_pair<kFmt, true>(x, w, p, stream, pdl)
-                                          : launch_fp4_pair<kFmt, false>(x, w, p, stream, pdl);
+        return launch_fp4_skinny<kFmt, 128, false>(x, nullptr, w, p, stream);
+    return p.N % 8 == 0 && aligned16(p.y) ? launch_fp4_pair<kFmt, true>(x, w, p, stream)
+                                          : launch_fp4_pair<kFmt, false>(x, w, p, stream);
 }
 
 fp4::GemmParams fp4_gemm_params(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
@@ -278,12 +285,12 @@ fp4::GemmParams fp4_gemm_params(const Fp4Operand &x, int64_t M, int64_t K, const
 }
 
 w8a8_status_t launch_fp4_gemm(const Fp4Operand &x, int64_t M, int64_t K, const w8a8_fp4_weight_t *w,
-                              const uint16_t *bias, uint16_t *y, cudaStream_t stream, bool pdl)
+                              const uint16_t *bias, uint16_t *y, cudaStream_t stream)
 {
     const fp4::GemmParams p = fp4_gemm_params(x, M, K, w, bias, y);
     const Fp4Operand wo{w->codes, w->scales, w->factor};
-    return w->format == W8A8_FP4_MX ? launch_fp4_gemm_t<fp4::kMx>(x, wo, p, stream, pdl)
-                                    : launch_fp4_gemm_t<fp4::kNv>(x, wo, p, stream, pdl);
+    return w->format == W8A8_FP4_MX ? launch_fp4_gemm_t<fp4::kMx>(x, wo, p, stream)
+                                    : launch_fp4_gemm_t<fp4::kNv>(x, wo, p, stream);
 }
 
 // The linear of at most fp4::kQuantRows rows: quantization and product in one kernel.
@@ -293,8 +300,8 @@ w8a8_status_t launch_fp4_linear_few(const uint16_t *x, int64_t M, int64_t K, con
     const fp4::GemmParams p = fp4_gemm_params(Fp4Operand{}, M, K, w, bias, y);
     const Fp4Operand wo{w->codes, w->scales, w->factor};
     return w->format == W8A8_FP4_MX
-               ? launch_fp4_skinny<fp4::kMx, 16, true>(Fp4Operand{}, x, wo, p, stream, false)
-               : launch_fp4_skinny<fp4::kNv, 16, true>(Fp4Operand{}, x, wo, p, stream, false);
+               ? launch_fp4_skinny<fp4::kMx, 16, true>(Fp4Operand{}, x, wo, p, stream)
+               : launch_fp4_skinny<fp4::kNv, 16, true>(Fp4Operand{}, x, wo, p, stream);
 }
 
 // A weight record: consistent fields; the buffers are checked by whoever uses them.

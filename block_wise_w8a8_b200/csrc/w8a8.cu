@@ -1126,7 +1126,7 @@ w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
                         ? reinterpret_cast<float *>(scales + fp4_scale_bytes(M, K, w->format))
                         : nullptr;
     W8A8_TRY(launch_fp4_quantize(x, M, K, w->format, codes, scales, factor, st));
-    W8A8_TRY(launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, st, true));
+    W8A8_TRY(launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, st));
     if (path_taken != nullptr)
         *path_taken = W8A8_PATH_FP4;
     return W8A8_OK;
@@ -1149,8 +1149,7 @@ w8a8_status_t w8a8_fp4_linear_prequant(const uint8_t *codes, const uint8_t *scal
     W8A8_TRY(check_device_ptr(y));
     if (bias != nullptr)
         W8A8_TRY(check_device_ptr(bias));
-    return launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, static_cast<cudaStream_t>(stream),
-                           false);
+    return launch_fp4_gemm(Fp4Operand{codes, scales, factor}, M, K, w, bias, y, static_cast<cudaStream_t>(stream));
 }
 
 w8a8_status_t w8a8_block_norm(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,

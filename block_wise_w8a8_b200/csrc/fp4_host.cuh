@@ -3,6 +3,10 @@
 // after the helpers it shares (device table, pointer checks, make_map).
 
 // ------------------------------------------------------------------ sizes and checks
+// Longest row of the 4-bit operators and of the block norm: offsets inside a row, 8 bytes of
+// scale tiles a value at the most, stay below 2^32.
+constexpr int64_t kMaxRowK = int64_t{1} << 24;
+
 bool fp4_format_ok(int format) { return format == W8A8_FP4_MX || format == W8A8_FP4_NV; }
 
 size_t fp4_scale_bytes(int64_t rows, int64_t K, int format)
@@ -28,7 +32,7 @@ w8a8_status_t fp4_shape(int64_t rows, int64_t K)
 {
     if (rows < 0 || K < 0)
         return W8A8_ERR_INVALID_ARG;
-    if (K == 0 || K % 32 || rows > kMaxTmaCoord || K > kMaxTmaCoord)
+    if (K == 0 || K % 32 || K > kMaxRowK || rows > kMaxTmaCoord)
         return W8A8_ERR_SHAPE;
     return W8A8_OK;
 }
@@ -397,7 +401,7 @@ w8a8_status_t block_norm_common(const uint16_t *h, const uint16_t *y, int post_n
     if (M < 0 || K < 0 || T <= 0 || !(eps >= 0.0f) || !(eps <= 3.4e38f) || !(res_scale >= -3.4e38f) ||
         !(res_scale <= 3.4e38f) || (post_gamma != nullptr && !post_norm))
         return W8A8_ERR_INVALID_ARG;
-    if (K == 0 || K % 8 || M % T || M > kMaxTmaCoord || K > kMaxTmaCoord)
+    if (K == 0 || K % 8 || M % T || K > kMaxRowK || M > kMaxTmaCoord)
         return W8A8_ERR_SHAPE;
     if (M == 0)
         return W8A8_OK;

@@ -1027,7 +1027,7 @@ w8a8_status_t w8a8_rowwise_linear(const int8_t *xq, const float *xs, int64_t M, 
 
 size_t w8a8_fp4_scale_bytes(int64_t rows, int64_t K, int format)
 {
-    if (rows <= 0 || K <= 0 || K % 32 || !fp4_format_ok(format))
+    if (rows <= 0 || K <= 0 || K % 32 || K > kMaxRowK || !fp4_format_ok(format))
         return 0;
     return fp4_scale_bytes(rows, K, format);
 }
@@ -1072,7 +1072,7 @@ w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, c
 
 size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format)
 {
-    if (M <= fp4::kQuantRows || K <= 0 || K % 32 || !fp4_format_ok(format))
+    if (M <= fp4::kQuantRows || K <= 0 || K % 32 || K > kMaxRowK || !fp4_format_ok(format))
         return 0;
     return round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2)) + fp4_scale_bytes(M, K, format) +
            (format == W8A8_FP4_NV ? static_cast<size_t>(M) * sizeof(float) : 0);
@@ -1097,7 +1097,7 @@ w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
     W8A8_TRY(check_device_ptr(y));
     if (bias != nullptr)
         W8A8_TRY(check_device_ptr(bias));
-    const bool four = K > 0 && K % 32 == 0 && K <= kMaxTmaCoord && M <= kMaxTmaCoord && N <= kMaxTmaCoord &&
+    const bool four = K > 0 && K % 32 == 0 && K <= kMaxRowK && M <= kMaxTmaCoord && N <= kMaxTmaCoord &&
                       w->codes != nullptr && aligned16(x);
     if (!four) {
         if (w->w_bf16 == nullptr && K > 0)

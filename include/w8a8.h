@@ -318,12 +318,13 @@ W8A8_API w8a8_status_t w8a8_rowwise_linear(const int8_t *xq, const float *xs, in
  *   exact.  A value that rounds to zero has code 0 or 8 (-0).  A value is code * scale (* factor).  Infinities and NaN: the block's scale is
  *   NaN (MX), the row's factor is NaN (NV), their codes 0.
  *
- * Layout of a quantized matrix [rows, K], K a positive multiple of 32:
+ * Layout of a quantized matrix [rows, K], K a positive multiple of 32 up to 2^24:
  *   codes  [rows, K/2] bytes, element 2 i in the low half of byte i;
  *   scales w8a8_fp4_scale_bytes(rows, K, format) bytes: 512-byte tiles of 128 rows x 4 blocks,
  *          tile (row / 128, block / 4) of [ceil(rows/128), ceil(blocks/4)], byte
  *          16 (row % 32) + 4 (row % 128 / 32) + block % 4.  The bytes of blocks past the end
- *          of K must be 0 (the quantizer writes 0 there and in rows past the end);
+ *          of K must be 0 (the quantizer writes 0 there and in rows past the end); E4M3 bytes
+ *          are below 128 (no sign);
  *   factor [rows] FP32 (NV), NULL (MX).
  * codes and scales 16-byte aligned, factor 4-byte aligned. */
 typedef enum {
@@ -348,7 +349,8 @@ typedef struct {
 W8A8_API size_t w8a8_fp4_scale_bytes(int64_t rows, int64_t K, int format);
 
 /* x [rows, K] BF16 -> codes, scales, factor (activations on every call, weights once).
- *   K a positive multiple of 32 (else W8A8_ERR_SHAPE); any rows >= 0; x 16-byte aligned.
+ *   K a positive multiple of 32 up to 2^24 (else W8A8_ERR_SHAPE); any rows >= 0; x 16-byte
+ *   aligned.
  *   A row's result depends on that row alone. */
 W8A8_API w8a8_status_t w8a8_fp4_quantize(const w8a8_bf16_t *x, int64_t rows, int64_t K, int format,
                                          uint8_t *codes, uint8_t *scales, float *factor,
@@ -368,7 +370,7 @@ W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format
 /* Y[M, N] = X[M, K] W^T + bias with X quantized in the call to the weight's format:
  *     y[m,n] = bf16( factor_x[m] factor_w[n] * sum_k value_x[m,k] value_w[n,k] + bias[n] ),
  *   values without factors, FP32 accumulation, one rounding to BF16; the sum's order is fixed
- *   by M, N and K.  Guard: the 4-bit path runs iff K is a positive multiple of 32, the weight
+ *   by M, N and K.  Guard: the 4-bit path runs iff K is a multiple of 32 up to 2^24, the weight
  *   has codes and x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and
  *   without that copy the call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M
  *   and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,
@@ -396,7 +398,7 @@ W8A8_API w8a8_status_t w8a8_fp4_linear_prequant(const uint8_t *codes, const uint
  *   all in FP32 (statistics included), rounded at h' and n only.  post_gamma, pre_gamma [K]
  *   and gate, scale, shift [M/T, K] BF16, each NULL to leave its factor out (post_gamma
  *   needs post_norm).  h, y [M, K]; h_out [M, K] may be h itself, no other overlap.  K a
- *   positive multiple of 8, T > 0 dividing M (else W8A8_ERR_SHAPE; T <= 0 gives
+ *   positive multiple of 8 up to 2^24, T > 0 dividing M (else W8A8_ERR_SHAPE; T <= 0 gives
  *   W8A8_ERR_INVALID_ARG), eps >= 0 and finite, res_scale finite; all buffers 16-byte
  *   aligned.  A row of zeros with eps = 0 gives NaN, as the formula does. */
 W8A8_API w8a8_status_t w8a8_block_norm(const w8a8_bf16_t *h, const w8a8_bf16_t *y, int post_norm,

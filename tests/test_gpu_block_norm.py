@@ -45,7 +45,9 @@ def _check(t, h2, n, K, res_scale=1.0, post_norm=True, eps=1e-6):
     assert bool(((n.double() - nn).abs() <= tol).all()), float(((n.double() - nn).abs() - tol).max())
 
 
-SHAPES = [(1, 8, 1), (3, 24, 3), (2, 32, 1), (17, 512, 1), (9, 520, 3), (10, 1024, 5), (12, 1000, 2), (300, 2048, 2),
+# many rows of each length that the ring takes, and the few-row form's lengths
+SHAPES = [(9500, 24, 5), (9480, 512, 4), (4800, 1000, 3), (2400, 2048, 2), (1300, 4096, 1300), (1200, 2560, 1),
+          (700, 8192, 7), (640, 10400, 2), (1, 8, 1), (3, 24, 3), (2, 32, 1), (17, 512, 1), (9, 520, 3), (10, 1024, 5), (12, 1000, 2), (300, 2048, 2),
           (7, 2080, 7), (130, 4096, 2), (5, 4104, 1), (6, 8192, 2), (3, 8200, 1), (4, 16384, 4), (2, 16392, 1),
           (3, 16416, 3), (2, 40000, 1), (2, 40008, 2)]
 
@@ -79,7 +81,8 @@ def test_left_out_factors(post, gammas, mod):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("M,K,B", [s for s in SHAPES if s[1] % 32 == 0] + [(131, 96, 1), (1400, 320, 7)])
+@pytest.mark.parametrize("M,K,B", [s for s in SHAPES if s[1] % 32 == 0] + [(131, 96, 1), (9700, 320, 10),
+                                                                          (4801, 992, 1)])
 def test_fp4_output_is_the_two_calls(fmt, M, K, B):
     t = _inputs(M, K, B, M * 3 + K)
     h2, n = w8.block_norm(**t, res_scale=1.25)
@@ -88,6 +91,25 @@ def test_fp4_output_is_the_two_calls(fmt, M, K, B):
     assert _same(h4, h2)
     assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
     assert q.factor is None or torch.equal(q.factor, want.factor)
+
+
+def test_offsets_past_32_bits():
+    M, K = 530000, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn((1000, K), generator=g, device="cuda").bfloat16().repeat(M // 1000, 1)
+    y = h.flip(1)
+    y[-5:] = torch.randn((5, K), generator=g, device="cuda").bfloat16()
+    gamma = torch.randn((K,), generator=g, device="cuda").bfloat16()
+    h2, n = w8.block_norm(h, y, post_gamma=gamma, pre_gamma=gamma)
+    assert h.numel() > 2 ** 31
+    for r in (0, 524287, 524288, M - 5, M - 1):
+        t = dict(h=h[r:r + 1], y=y[r:r + 1], post_gamma=gamma, pre_gamma=gamma, gate=None, scale=None, shift=None)
+        _check(t, h2[r:r + 1], n[r:r + 1], K)
+    h4, q = w8.block_norm_fp4(h, y, "nvfp4", post_gamma=gamma, pre_gamma=gamma, h_out=h)
+    assert _same(h4[-5:], h2[-5:])
+    want = w8.fp4_quantize(n[-5:].contiguous())
+    assert torch.equal(q.codes[-5:], want.codes)
+    assert torch.equal(ref.plain_scales(q)[-5:], ref.plain_scales(want))
 
 
 def test_zero_rows_and_infinities():

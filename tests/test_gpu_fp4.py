@@ -227,6 +227,94 @@ def test_large_product_on_sampled_rows():
         assert bool((err <= want.abs() * 2.0 ** -8 + size * (K / 64 + 8) * 2.0 ** -22).all()), fmt
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_offsets_past_32_bits(fmt):
+    """More than 2^31 elements of x and of y: the last rows are those of a call of their own."""
+    M, K = 280000, 8192
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((256, K), generator=g, device="cuda").bfloat16().repeat((M + 255) // 256, 1)[:M].contiguous()
+    x[-300:] = torch.randn((300, K), generator=g, device="cuda").bfloat16()
+    q = w8.fp4_quantize(x, fmt)
+    y = w8.fp4_dequantize(q)
+    one = w8.fp4_quantize(x[-300:].contiguous(), fmt)
+    assert torch.equal(q.codes[-300:], one.codes)
+    assert torch.equal(ref.plain_scales(q)[-300:], ref.plain_scales(one))
+    assert torch.equal(y[-300:].view(torch.int16), w8.fp4_dequantize(one).view(torch.int16))
+    del x, y, q
+    M, K = 70000, 256
+    for N in (40000, 39999):
+        x = _random_weight(M, K, fmt, 7)
+        w = _random_weight(N, K, fmt, 8)
+        y = w8.fp4_linear_prequant(x, w8.FP4Weight(q=w))
+        assert y.numel() > 2 ** 31
+        rows = torch.tensor([0, 1, 53687, 53688, M - 257, M - 1], device="cuda")
+        xv = ref.tensor_values(x)[rows]
+        wv = ref.tensor_values(w)
+        want, size = xv @ wv.T, xv.abs() @ wv.abs().T
+        err = (y[rows].double() - want).abs()
+        assert bool((err <= want.abs() * 2.0 ** -8 + size * (K / 64 + 8) * 2.0 ** -22).all()), N
+        del y
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_output_at_any_even_address(fmt):
+    """An output that starts two bytes past a 16-byte boundary, and a bias and factors that
+    start anywhere their type may: the same bits as aligned ones."""
+    for M, K, N in [(5, 256, 264), (300, 288, 520)]:
+        x, w = _random_weight(M, K, fmt, 1), _random_weight(N, K, fmt, 2)
+        bias = torch.randn((N + 1,), generator=_gen(3)).bfloat16().cuda()
+        want = w8.fp4_linear_prequant(x, w8.FP4Weight(q=w), bias[1:].clone())
+        flat = torch.full((M * N + 9,), 3.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[1:1 + M * N].view(M, N)
+        if fmt == "nvfp4":
+            big = torch.zeros((N + 1,), device="cuda")
+            big[1:] = w.factor
+            w = w8.FP4Tensor(w.codes, w.scales, big[1:], fmt)
+        w8.fp4_linear_prequant(x, w8.FP4Weight(q=w), bias[1:], out=out)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        assert float(flat[0]) == 3 and bool((flat[1 + M * N:] == 3).all())
+
+
+def test_one_dimension_and_empty_leading():
+    wt = w8.FP4Weight(torch.randn((40, 96), generator=_gen(1)).bfloat16().cuda())
+    x = torch.randn((3, 96), generator=_gen(2)).bfloat16().cuda()
+    y = w8.fp4_linear(x, wt)
+    assert torch.equal(w8.fp4_linear(x[1], wt).view(torch.int16), w8.fp4_linear(x[1:2], wt)[0].view(torch.int16))
+    assert w8.fp4_linear(x.view(1, 3, 1, 96), wt).shape == (1, 3, 1, 40) and y.shape == (3, 40)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_few_rows_quantized_in_the_product(fmt):
+    """1 to 5 rows on both sides of the quantizing product's limit, K from one block pair to
+    several splits, rows of zeros and of very different sizes: the bits of the two calls."""
+    for K, N in [(32, 1), (96, 130), (288, 100), (2080, 520), (4096, 4096), (16416, 136)]:
+        w = w8.FP4Weight((torch.randn((N, K), generator=_gen(K)) * K ** -0.5).bfloat16().cuda(), fmt, keep_bf16=False)
+        b = torch.randn((N,), generator=_gen(N)).bfloat16().cuda()
+        x = (torch.randn((5, K), generator=_gen(5)) * torch.tensor([1, 300, 1e-4, 0, 7])[:, None]).bfloat16().cuda()
+        for M in range(1, 6):
+            y = w8.fp4_linear(x[:M], w, b)
+            want = w8.fp4_linear_prequant(w8.fp4_quantize(x[:M], fmt), w, b)
+            assert torch.equal(y.view(torch.int16), want.view(torch.int16)), (K, N, M)
+
+
+def test_two_streams_at_once():
+    """Calls of every kernel in flight on two streams: the bits of the calls one by one."""
+    g = _gen(12)
+    wt = [w8.FP4Weight((torch.randn((768, 1024), generator=g) / 32).bfloat16().cuda(), f) for f in FORMATS]
+    xs = [torch.randn((M, 1024), generator=g).bfloat16().cuda() for M in (1, 3, 20, 100, 900)]
+    want = [[w8.fp4_linear(x, w) for x in xs] for w in wt]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k] = [w8.fp4_linear(x, wt[k]) for x in xs]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u.view(torch.int16), v.view(torch.int16)) for u, v in zip(a, b))
+
+
 @pytest.mark.parametrize("M,K,N", [(3, 40, 16), (70, 1000, 65), (4, 0, 9)])
 def test_guard_takes_bf16(M, K, N):
     g = _gen(K)

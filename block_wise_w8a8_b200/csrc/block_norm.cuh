@@ -117,10 +117,16 @@ __device__ __forceinline__ float row_sum(float v, float *s, int warp, uint32_t l
         if (lane == 0)
             s[warp] = v;
         __syncthreads();
-        v = 0.0f;
+        if constexpr (W == 2) {
+            v = s[0] + s[1];
+        } else {
+            v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            v += s[i];
+            for (int i = 0; i < W; i += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(s + i);
+                v += (f.x + f.y) + (f.z + f.w);
+            }
+        }
     }
     return v;
 }
@@ -157,8 +163,8 @@ __device__ __forceinline__ void normalise(const Pre &c, float rstd, const uint32
 // Shared memory: the ring, `stages` slots of h and y of a row (4 K bytes), then this.
 template <int W>
 struct StreamTail {
-    float red[2][2][W];                  // by row parity and sum
-    uint32_t top[2][W];
+    alignas(16) float red[2][2][W];      // by row parity and sum
+    alignas(16) uint32_t top[2][W];
     uint64_t full[fp4::kMaxRing];
     int abort;
 };
@@ -202,22 +208,27 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
     Post post[kKeep ? P : 1];
     Pre pre[kKeep ? P : 1];
     const float inv_k = __fdiv_rn(1.0f, static_cast<float>(p.K));
-    int64_t group = -1;
+    // the rows' group: its offset in gate, scale and shift, and its end
+    int64_t mod = 0, group_end = 0;
     int s = 0, par = 0;
     uint32_t phase = 0;
     for (int64_t r = blockIdx.x; r < p.M; r += gridDim.x, par ^= 1) {
-        const int64_t g = r / p.T;
-        if (kKeep && g != group) {
+        const bool next_group = r >= group_end;
+        if (next_group) {
+            const int64_t g = r / p.T;
+            mod = g * p.K;
+            group_end = (g + 1) * p.T;
+        }
+        if (kKeep && next_group) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int b = b0 + i * kStep;
                 if (b < np) {
-                    load_post(p, b * 8, g * p.K, post[kKeep ? i : 0]);
-                    load_pre(p, b * 8, g * p.K, pre[kKeep ? i : 0]);
+                    load_post(p, b * 8, mod, post[kKeep ? i : 0]);
+                    load_pre(p, b * 8, mod, pre[kKeep ? i : 0]);
                 }
             }
         }
-        group = g;
         // A wait that gives up is recorded; the row is then worked on as it is, so that every
         // warp reaches every barrier.
         mbar_wait(&sm.full[s], phase, abort);
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             if (b < np) {
                 Post &f = post[kKeep ? i : 0];
                 if (!kKeep)
-                    load_post(p, b * 8, g * p.K, f);
+                    load_post(p, b * 8, mod, f);
                 update(f, p.res_scale, rstd, h[i], y[i]);
                 *reinterpret_cast<uint4 *>(h_row + b * 8) = pack4(y[i]);
                 add_squares(y[i], acc);
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             if (b < np) {
                 Pre &f = pre[kKeep ? i : 0];
                 if (!kKeep)
-                    load_pre(p, b * 8, g * p.K, f);
+                    load_pre(p, b * 8, mod, f);
                 normalise(f, rstd, y[i], h[i]);
                 if constexpr (kOut == kOutBf16)
                     *reinterpret_cast<uint4 *>(p.n_out + r * p.K + b * 8) = pack4(h[i]);
@@ -305,8 +316,8 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
 template <int kOut, int W, int P, bool kLong>
 __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
 {
-    __shared__ float s_red[2][W];
-    __shared__ uint32_t s_top[W];
+    __shared__ __align__(16) float s_red[2][W];
+    __shared__ __align__(16) uint32_t s_top[W];
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();

@@ -256,9 +256,15 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *s, int warp, u
         if (lane == 0)
             s[warp] = v;
         __syncthreads();
+        if constexpr (W == 2) {
+            v = max(s[0], s[1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            v = max(v, s[i]);
+            for (int i = 0; i < W; i += 4) {
+                const uint4 f = *reinterpret_cast<const uint4 *>(s + i);
+                v = max(v, max(max(f.x, f.y), max(f.z, f.w)));
+            }
+        }
     }
     return v;
 }
@@ -293,7 +299,7 @@ __device__ __forceinline__ void zero_scales(uint8_t *scales, int64_t rows, int64
 template <int kFmt, int W, int P>
 __global__ void __launch_bounds__(W * 32) quantize_kernel(const QParams p)
 {
-    __shared__ uint32_t s_top[W];
+    __shared__ __align__(16) uint32_t s_top[W];
     asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
@@ -365,7 +371,7 @@ constexpr int kStreamWarps = 32;                 // warps a SM
 constexpr int kMaxRing = 16;                     // rows of a ring at most
 template <int W>
 struct StreamTail {                              // behind the ring
-    uint32_t top[2][W];                          // by row parity
+    alignas(16) uint32_t top[2][W];              // by row parity
     uint64_t full[kMaxRing];
     int abort;
 };

@@ -263,11 +263,13 @@ w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const 
         return launch_fp4_skinny<kFmt, 32, false>(x, nullptr, w, p, stream);
     if (p.M <= 64)
         return launch_fp4_skinny<kFmt, 64, false>(x, nullptr, w, p, stream);
-    // From 65 tokens on the pair kernel is the faster one where its tiles fill enough of the
-    // device: 128 x 4096 x 16384 15.2 us for 18.3, 128 x 2048 x 8192 10.5 for 13.3; but
-    // 128 x 4096 x 4096, 16 tiles that it does not split along K, 12.3 for 11.5 and
-    // 128 x 16384 x 4096 27.4 for 18.9.
-    if (p.M <= 128 && p.N <= 4096)
+    // From 65 tokens on pairs of CTAs, which do not split K, unless the output is so small and K
+    // so long that there are no more 128 x 128 tiles than slices of K: 1000 x 16384 x 8 20.1
+    // -> 10.0 us, 256 x 16384 x 4096 (64 tiles, 64 slices) 23.0 -> 20.2; on the other side
+    // 300 x 4096 x 1024 (24, 16) 8.9 us with pairs, 10.4 split, 2000 x 8192 x 512 (64, 32)
+    // 13.0 and 14.8.
+    const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
+    if (tiles <= p.slices)
         return launch_fp4_skinny<kFmt, 128, false>(x, nullptr, w, p, stream);
     return p.N % 8 == 0 && aligned16(p.y) ? launch_fp4_pair<kFmt, true>(x, w, p, stream)
                                           : launch_fp4_pair<kFmt, false>(x, w, p, stream);

@@ -147,7 +147,8 @@ def _check_product(y, xq, wq, bias, what):
 SHAPES = [(1, 32, 1), (1, 64, 130), (5, 96, 128), (16, 256, 256), (17, 288, 100), (31, 544, 257), (33, 1024, 129),
           (64, 2048, 384), (65, 160, 40), (100, 4096, 200), (128, 512, 512), (3, 8192, 24)]
 LARGE = [(129, 64, 8), (129, 32, 1), (256, 256, 256), (257, 288, 255), (300, 544, 520), (512, 1056, 1000),
-         (1000, 2048, 777), (640, 4096, 2056), (2100, 320, 3000)]
+         (1000, 2048, 777), (640, 4096, 2056), (2100, 320, 3000),
+         (1000, 16384, 8), (300, 8192, 1001), (70, 2048, 300), (19000, 96, 264)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

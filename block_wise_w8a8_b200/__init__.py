@@ -584,13 +584,13 @@ class FP4Tensor:
 
 
 def _fp4_empty(rows, K, format, device):
-    """A quantized matrix of this size, to be written: codes, scales (16-byte aligned) and
-    factors in one allocation."""
+    """A quantized matrix of this size, to be written: codes, scales (from a 256-byte boundary,
+    where the TMA reads them fastest) and factors in one allocation."""
     _fp4_k(K)
     q = FP4Tensor.__new__(FP4Tensor)
     q.rows, q.K, q.format, q.device, q._parts = rows, K, format, device, None
     rt, ct, _ = _fp4_tiles(rows, K, format)
-    at = (rows * K // 2 + 15) // 16 * 16
+    at = (rows * K // 2 + 255) // 256 * 256
     end = at + rt * ct * 512
     nv = format == "nvfp4"
     q._buffer = torch.empty(end + 4 * rows if nv else end, dtype=torch.uint8, device=device)

@@ -70,14 +70,26 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
 #undef W8A8_FP4_MMA
 }
 
-// 512-byte scale tile, shared -> tensor memory: 32 rows of 16 bytes to lanes 0-31 (and the
-// same to lanes 32-63, 64-95, 96-127) of 4 columns.  The descriptor: no swizzle, 8-row
-// groups 128 bytes apart.
-template <int kCtas>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
+// Shared-memory matrix descriptors in two words, so that a step's only arithmetic is on the
+// low one: the address >> 4 (bit 16: a leading offset of 1, unused).  High words: operands in
+// 128-byte rows, swizzled, 8-row groups 1024 bytes apart; scale tiles of 32 rows of 16 bytes,
+// not swizzled, 8-row groups 128 bytes apart.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kScaleHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t operand_lo(const void *p) { return (smem_u32(p) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi)
 {
-    const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
-                       (static_cast<uint64_t>(1u) << 46);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
+// 512-byte scale tile, shared -> tensor memory: its 32 rows of 16 bytes to lanes 0-31 (and the
+// same to lanes 32-63, 64-95, 96-127) of 4 columns.
+template <int kCtas>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo)
+{
+    const uint64_t d = desc_of(lo, kScaleHi);
     if constexpr (kCtas == 1)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
     else
@@ -85,9 +97,9 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
 }
 
 // One lane of the converged warp.  The tcgen05 and TMA instructions below are issued under
-// this predicate, with the control flow and the operands around them the same in all lanes:
-// the compiler then keeps operands in uniform registers.  Issued by a thread picked with
-// lane == 0, each took about 60 cycles, 16 a slice against the 512 cycles of its products.
+// this predicate: the compiler then takes the code for one thread's and keeps operands in
+// uniform registers.  Issued by a thread picked with lane == 0, each took about 60 cycles,
+// 17 a slice against the 512 cycles of its products.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;
@@ -105,20 +117,26 @@ __device__ __forceinline__ bool elect_one()
 //
 // kTma: four epilogue warps, 64 columns at a time through shared memory to TMA stores.
 // Otherwise (N not a multiple of 8, or y not 16-byte aligned, where no TMA store can go) the
-// rows of y start at any even address and are stored two bytes a lane, which costs more
+// rows of y start at any even address and are stored two bytes a lane, which takes more
 // instructions; eight warps share them, two to the 32 rows of tensor memory that a warp may
-// read, 32 columns at a time (1000 x 2016 x 8191: 22 us, with four warps 30).  With TMA
-// eight warps are slower, 427 us for 407 at 16384 x 4096 x 16384.
+// read, 32 columns at a time (1000 x 2016 x 8191: 18 us, with four warps 30; with N = 8192 and
+// TMA 14.8).  With TMA eight warps are slower, 427 us for 407 at 16384 x 4096 x 16384.
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit in 512 columns,
 // so the accumulators share columns: one at 0, the other ending where the scales begin.
-// The warps that read the shared columns read them first, and then the next tile's
-// products start, so only that first read is not overlapped.
+// The warps that read the shared columns read them first, into registers, and then the next
+// tile's products start, so only that first read is not overlapped.  A slice's scales are
+// copied over those of the slice before the last, whose products have then completed:
+// tcgen05.cp is ordered before the products issued after it, but not after those before it.
 //
 // The tiles of a last, partial round are cut in half along N when the halves fit in one
 // round: 256 x 4096 x 4096, 16 tiles on 74 pairs, 11.1 -> 8.9 us; 4096^3 (mxfp4), 3.5 rounds
-// in place of 4, 33.9 -> 32.2 us.  With kTma only: a number of steps known at run time costs
-// the other epilogue more (1000 x 2016 x 8191 17.6 -> 20.8 us).
+// in place of 4, 33.9 -> 32.2 us.  With kTma only.
+//
+// 16384 x 4096 x 16384: 409 us in a burst (81% of four times the BF16 rate), 465 back to back
+// under the power cap (sw_power_cap; SM clock about 1.5 GHz); 8192^3 185 us (90%), mxfp4 175
+// (95%).  Bound by the products: a tile takes 9350 cycles, 8192 of them its products at the
+// full rate.
 constexpr int kPairStages = 5;
 constexpr int kPairGroup = 8;                // M tiles of a raster group
 
@@ -152,9 +170,10 @@ struct alignas(1024) PairSmem {
 template <int kFmt, bool kTma>
 constexpr size_t kPairSmemBytes = sizeof(PairSmem<kFmt, kTma>) + 1024;
 
-// Tensor memory columns of the pair kernel: SFA and SFB of one slice at the end.
+// Tensor memory columns of the pair kernel: SFA and SFB of two slices at the end, by slice
+// parity, and the second accumulator before them.
 __host__ __device__ constexpr uint32_t pair_sf_cols(int fmt) { return 12u * scale_tiles_a_slice(fmt); }
-__host__ __device__ constexpr uint32_t pair_acc1(int fmt) { return 512u - pair_sf_cols(fmt) - 256u; }
+__host__ __device__ constexpr uint32_t pair_acc1(int fmt) { return 512u - 2 * pair_sf_cols(fmt) - 256u; }
 
 __device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank)
 {
@@ -202,6 +221,37 @@ __device__ __forceinline__ void pair_unit(int u, const GemmParams &p, int &tm, i
     const int local = t - group * per_group;
     tm = first + local % gsz;
     tn = local / gsz;
+}
+
+// 32 rows x 32 BF16 of a warp's staging buffer (gemm::stage_off) to y, one column a lane; row
+// pointers by addition, four in turn.
+__device__ __forceinline__ void store_rows(uint16_t *y, int64_t N, const uint8_t *out, int rows, bool in, int lane)
+{
+    const uint8_t *src[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        src[k] = out + (lane & 7) * 2 + (((lane >> 3) ^ k) << 4);
+    uint16_t v[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+        v[r] = *reinterpret_cast<const uint16_t *>(src[(r >> 1) & 3] + r * 64);
+    if (!in)
+        return;
+    uint16_t *d[4] = {y, y + N, y + 2 * N, y + 3 * N};
+    if (rows == 32) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            *d[r & 3] = v[r];
+            d[r & 3] += 4 * N;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            if (r < rows)
+                *d[r & 3] = v[r];
+            d[r & 3] += 4 * N;
+        }
+    }
 }
 
 template <int kFmt, bool kTma>
@@ -305,60 +355,73 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
-            const uint32_t sfa = tmem + 512 - pair_sf_cols(kFmt);
-            const uint32_t sfb = sfa + 4 * kTiles;
-            uint32_t it = 0, i = 0;
-            bool ok = true;
-            for (int t = pair; ok && t < num_units; t += pairs, ++i) {
-                const bool whole = t < p.num_full;
-                // tile i - 2 has left this accumulator, tile i - 1 the columns both use
-                if (i > 1 && !gemm::gemm_wait(&sm.tdrained[i & 1], ((i >> 1) - 1) & 1, abort))
-                    break;
-                if (i > 0 && !gemm::gemm_wait(&sm.tshared, (i - 1) & 1, abort))
-                    break;
-                tc_fence_after();
-                const uint32_t d = tmem + (i & 1) * pair_acc1(kFmt);
-                for (int ks = 0; ks < p.slices; ++ks, ++it) {
-                    const uint32_t s = it % kPairStages, ph = (it / kPairStages) & 1;
-                    if (!gemm::gemm_wait(&sm.full[s], ph, abort)) {
-                        ok = false;
+            // One thread issues everything; a slice's 17 instructions and its two waits have to
+            // fit the 512 cycles of its products, so ring positions and descriptors are counted
+            // on, not computed.
+            if (elect_one()) {
+                const uint32_t a0 = operand_lo(sm.a[0]), b0 = operand_lo(sm.b[0]);
+                const uint32_t fa0 = smem_u32(sm.sfa[0]) >> 4, fb0 = smem_u32(sm.sfb[0][0]) >> 4;
+                uint32_t i = 0, it = 0;
+                uint32_t s = 0, ph = 0;                              // slice it in the ring
+                uint32_t s2 = kPairStages - 2, ph2 = 1;              // slice it - 2
+                bool ok = true;
+                for (int t = pair; ok && t < num_units; t += pairs, ++i) {
+                    const bool whole = t < p.num_full;
+                    // tile i - 2 has left this accumulator, tile i - 1 the columns both use
+                    if (i > 1 && !gemm::gemm_wait(&sm.tdrained[i & 1], ((i >> 1) - 1) & 1, abort))
                         break;
-                    }
+                    if (i > 0 && !gemm::gemm_wait(&sm.tshared, (i - 1) & 1, abort))
+                        break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t fa = smem_u32(sm.sfa[s]), fb0 = smem_u32(sm.sfb[s][0]), fb1 = smem_u32(sm.sfb[s][1]);
+                    const uint32_t d = tmem + (i & 1) * pair_acc1(kFmt);
+                    for (int ks = 0; ks < p.slices; ++ks, ++it) {
+                        // the products of slice it - 2 have read the scales that this one replaces
+                        if ((it >= 2 && !gemm::gemm_wait(&sm.empty[s2], ph2, abort)) ||
+                            !gemm::gemm_wait(&sm.full[s], ph, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sfa = tmem + 512 - (1 + (it & 1)) * pair_sf_cols(kFmt);
+                        const uint32_t sfb = sfa + 4 * kTiles;
+                        const uint32_t fa = fa0 + s * (kSfBytes >> 4), fb = fb0 + s * (2 * kSfBytes >> 4);
+                        const uint32_t a = a0 + s * (128 * 128 >> 4), b = b0 + s * (128 * 128 >> 4);
 #pragma unroll
                         for (int j = 0; j < kTiles; ++j) {
-                            copy_scales<2>(sfa + 4 * j, fa + 512 * j);
-                            copy_scales<2>(sfb + 8 * j, fb0 + 512 * j);
+                            copy_scales<2>(sfa + 4 * j, fa + (512 >> 4) * j);
+                            copy_scales<2>(sfb + 8 * j, fb + (512 >> 4) * j);
                             if (whole)
-                                copy_scales<2>(sfb + 8 * j + 4, fb1 + 512 * j);
+                                copy_scales<2>(sfb + 8 * j + 4, fb + (kSfBytes >> 4) + (512 >> 4) * j);
                         }
-                        const uint64_t ad = umma_desc_sw128(smem_u32(sm.a[s]));
-                        const uint64_t bd = umma_desc_sw128(smem_u32(sm.b[s]));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int j = kFmt == kMx ? k >> 1 : k;
-                            constexpr int cut_n = 128;
                             const int sf = kFmt == kMx ? (k & 1) * 2 : 0;
-                            const uint32_t id = whole ? idesc_fp4(256, 256, kFmt, sf) : idesc_fp4(256, cut_n, kFmt, sf);
-                            umma_fp4<kFmt, 2>(d, ad + 2 * k, bd + 2 * k, id, sfa + 4 * j, sfb + 8 * j, (ks | k) != 0);
+                            const uint32_t id = whole ? idesc_fp4(256, 256, kFmt, sf) : idesc_fp4(256, 128, kFmt, sf);
+                            umma_fp4<kFmt, 2>(d, desc_of(a + 2 * k, kOperandHi), desc_of(b + 2 * k, kOperandHi), id,
+                                              sfa + 4 * j, sfb + 8 * j, (ks | k) != 0);
                         }
                         commit_pair(&sm.empty[s]);
                         if (ks == p.slices - 1)
                             commit_pair(&sm.tfull[i & 1]);
+                        if (++s == kPairStages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
+                        if (++s2 == kPairStages) {
+                            s2 = 0;
+                            ph2 ^= 1;
+                        }
                     }
-                    __syncwarp();
                 }
-            }
-            // every product issued here completes before tensor memory is released
-            if (elect_one())
+                // every product issued here completes before tensor memory is released
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                                  smem_u32(&sm.mma_done))
                              : "memory");
+                volatile int no_abort = 0;
+                mbar_wait(&sm.mma_done, 0, &no_abort, 100000000ull);
+            }
             __syncwarp();
-            volatile int no_abort = 0;
-            mbar_wait(&sm.mma_done, 0, &no_abort, 100000000ull);
         }
     } else {
         // ---------------------------------------------------------------- epilogue
@@ -368,6 +431,17 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * E::kWidth;
         const uint32_t shared = map_to(smem_u32(&sm.tshared), 0);
         const uint32_t drained = map_to(smem_u32(&sm.tdrained[0]), 0);
+        using Chunk = uint32_t[E::kChunk / 32][32];
+        auto load_chunk = [](uint32_t taddr, Chunk &r) {
+#pragma unroll
+            for (int q = 0; q < E::kChunk / 32; ++q)
+                tmem_ld32(taddr + q * 32, r[q]);
+        };
+        auto wait_chunk = [](Chunk &r) {
+#pragma unroll
+            for (int q = 0; q < E::kChunk / 32; ++q)
+                tmem_wait_ld(r[q]);
+        };
         uint8_t *out = sm.out[ew];
         float *wf = sm.col[ew][0], *bias = sm.col[ew][1];
         uint32_t i = 0;
@@ -394,33 +468,13 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                 break;
             tc_fence_after();
             const uint32_t acc = lane_base + buf * pair_acc1(kFmt);
-            // The columns that both accumulators use, the last 48 (kMx: 24) of the lower one and
-            // the first of the upper one, come first: in 64 columns, from one end or the other.
-            constexpr int kSharedSteps = 64 / E::kChunk;
-            static_assert(pair_sf_cols(kFmt) <= 64, "shared columns");
+            // The columns that both accumulators use (kNv: 96, kMx: 48) are the last of the lower
+            // one and the first of the upper one.  A warp's first steps, from that end (two of 64
+            // or three of 32), are read into registers at once; with them the shared columns are
+            // free, and with the rest the accumulator.
+            static_assert(2 * pair_sf_cols(kFmt) <= 96, "shared columns");
             const bool holds_shared = E::kParts == 1 || part != static_cast<int>(buf);
-#pragma unroll 1
-            for (int step = 0; step < steps; ++step) {
-                const int c = buf == 0 ? steps - 1 - step : step;
-                uint32_t r[E::kChunk / 32][32];
-#pragma unroll
-                for (int q = 0; q < E::kChunk / 32; ++q)
-                    tmem_ld32(acc + c * E::kChunk + q * 32, r[q]);
-#pragma unroll
-                for (int q = 0; q < E::kChunk / 32; ++q)
-                    tmem_wait_ld(r[q]);
-                if (step == kSharedSteps - 1 && holds_shared) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        arrive_remote(shared);
-                }
-                if (step == steps - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        arrive_remote(drained + buf * 8);
-                }
+            auto store_chunk = [&](const Chunk &r, int c0) {
                 if (kTma && lane == 0)
                     gemm::tma_store_wait_read();
                 __syncwarp();
@@ -430,8 +484,8 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int e = g * 8 + q * 2;
-                        const float2 f = *reinterpret_cast<const float2 *>(wf + c * E::kChunk + e);
-                        const float2 b = *reinterpret_cast<const float2 *>(bias + c * E::kChunk + e);
+                        const float2 f = *reinterpret_cast<const float2 *>(wf + c0 + e);
+                        const float2 b = *reinterpret_cast<const float2 *>(bias + c0 + e);
                         const float v0 = __uint_as_float(r[e >> 5][e & 31]), v1 = __uint_as_float(r[e >> 5][(e & 31) + 1]);
                         o[q] = kFmt == kNv ? pack_bf16x2(fmaf(v0, xf * f.x, b.x), fmaf(v1, xf * f.y, b.y))
                                            : pack_bf16x2(v0 + b.x, v1 + b.y);
@@ -439,7 +493,7 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                     st_shared_v4(out + (kTma ? lane * 128 + ((g ^ (lane & 7)) << 4) : gemm::stage_off(lane, g)),
                                  make_uint4(o[0], o[1], o[2], o[3]));
                 }
-                const int64_t nc = n0 + c * E::kChunk;
+                const int64_t nc = n0 + c0;
                 if (kTma) {
                     gemm::fence_proxy_async_smem();
                     __syncwarp();
@@ -447,22 +501,52 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                         gemm::tma_store_2d(&tmY, out, static_cast<int32_t>(nc), static_cast<int32_t>(m_w));
                 } else {
                     __syncwarp();
-                    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - m_w));
-                    if (nc + lane < p.N) {
-                        uint16_t *dst = p.y + m_w * p.N + nc + lane;
-                        const uint8_t *src = out + (lane & 7) * 2;
-#pragma unroll
-                        for (int r0 = 0; r0 < 32; r0 += 16) {
-                            uint16_t v[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                v[j] = *reinterpret_cast<const uint16_t *>(src + gemm::stage_off(r0 + j, lane >> 3));
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (r0 + j < rows)
-                                    dst[(r0 + j) * p.N] = v[j];
-                        }
+                    store_rows(p.y + m_w * p.N + nc + lane, p.N, out, static_cast<int>(min(static_cast<int64_t>(32), p.M - m_w)),
+                               nc + lane < p.N, static_cast<int>(lane));
+                }
+            };
+            auto column = [&](int step) { return (buf == 0 ? steps - 1 - step : step) * E::kChunk; };
+            auto arrive = [&](bool here, uint32_t bar) {
+                if (here && lane == 0)
+                    arrive_remote(bar);
+            };
+            if constexpr (kTma) {
+                Chunk r0, r1;
+                load_chunk(acc + column(0), r0);
+                load_chunk(acc + column(1), r1);
+                wait_chunk(r0);
+                wait_chunk(r1);
+                tc_fence_before();
+                __syncwarp();
+                arrive(true, shared);
+                arrive(steps == 2, drained + buf * 8);
+                store_chunk(r0, column(0));
+                if (steps == 4)
+                    load_chunk(acc + column(2), r0);
+                store_chunk(r1, column(1));
+                if (steps == 4) {
+                    load_chunk(acc + column(3), r1);
+                    wait_chunk(r0);
+                    wait_chunk(r1);
+                    tc_fence_before();
+                    __syncwarp();
+                    arrive(true, drained + buf * 8);
+                    store_chunk(r0, column(2));
+                    store_chunk(r1, column(3));
+                }
+            } else {
+#pragma unroll 1
+                for (int step = 0; step < 4; ++step) {
+                    const int c0 = column(step);
+                    Chunk r;
+                    load_chunk(acc + c0, r);
+                    wait_chunk(r);
+                    if ((step == 2 && holds_shared) || step == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        arrive(true, step == 3 ? drained + buf * 8 : shared);
                     }
+                    store_chunk(r, c0);
                 }
             }
         }
@@ -609,7 +693,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     constexpr int kStages = S::kStages;
     constexpr uint32_t kTxBytes =
         kQuant ? 128 * 128 + scale_slice_bytes(kFmt) : static_cast<uint32_t>(S::kStageBytes);
-    constexpr uint32_t kCols = BT + 8 * kTiles <= 64 ? 64 : (BT + 8 * kTiles <= 128 ? 128 : 256);
+    // the accumulator, and the scales of each stage
+    constexpr uint32_t kUsed = BT + kStages * 8 * kTiles;
+    constexpr uint32_t kCols = kUsed <= 128 ? 128 : 256;
+    static_assert(kUsed <= 256, "two CTAs share a SM's 512 columns");
     extern __shared__ uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -677,34 +764,40 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
                 ;
         }
     } else if (warp == 1) {
-        const uint32_t sfw = tmem + BT, sfx = sfw + 4 * kTiles;
-        uint32_t it = 0;
-        for (int ks = ks0; ks < ks1; ++ks, ++it) {
-            const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-            if (!gemm::gemm_wait(&sm.full[s], ph, abort))
-                break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t fw = smem_u32(sm.sfw[s]), fx = smem_u32(sm.sfx[s]);
+        if (elect_one()) {
+            const uint32_t w0 = operand_lo(sm.w[0]), x0 = operand_lo(sm.x[0]);
+            const uint32_t fw0 = smem_u32(sm.sfw[0]) >> 4, fx0 = smem_u32(sm.sfx[0]) >> 4;
+            uint32_t s = 0, ph = 0;
+            for (int ks = ks0; ks < ks1; ++ks) {
+                if (!gemm::gemm_wait(&sm.full[s], ph, abort))
+                    break;
+                tc_fence_after();
+                // a stage's scales have their own columns: they are free when the stage is
+                const uint32_t sfw = tmem + BT + s * (8 * kTiles), sfx = sfw + 4 * kTiles;
+                const uint32_t fw = fw0 + s * (scale_slice_bytes(kFmt) >> 4), fx = fx0 + s * (scale_slice_bytes(kFmt) >> 4);
+                const uint32_t w = w0 + s * (128 * 128 >> 4), x = x0 + s * (BT * 128 >> 4);
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
-                    copy_scales<1>(sfw + 4 * j, fw + 512 * j);
-                    copy_scales<1>(sfx + 4 * j, fx + 512 * j);
+                    copy_scales<1>(sfw + 4 * j, fw + (512 >> 4) * j);
+                    copy_scales<1>(sfx + 4 * j, fx + (512 >> 4) * j);
                 }
-                const uint64_t wd = umma_desc_sw128(smem_u32(sm.w[s]));
-                const uint64_t xd = umma_desc_sw128(smem_u32(sm.x[s]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int j = kFmt == kMx ? k >> 1 : k;
                     const uint32_t id = idesc_fp4(128, BT, kFmt, kFmt == kMx ? (k & 1) * 2 : 0);
-                    umma_fp4<kFmt, 1>(tmem, wd + 2 * k, xd + 2 * k, id, sfw + 4 * j, sfx + 4 * j, it != 0 || k != 0);
+                    umma_fp4<kFmt, 1>(tmem, desc_of(w + 2 * k, kOperandHi), desc_of(x + 2 * k, kOperandHi), id,
+                                      sfw + 4 * j, sfx + 4 * j, ks != ks0 || k != 0);
                 }
                 umma_commit(&sm.empty[s]);
                 if (ks == ks1 - 1)
                     umma_commit(&sm.tfull);
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            __syncwarp();
         }
+        __syncwarp();
     } else if (kQuant) {
         quantize_slices<kFmt>(sm, p, x, ks0, ks1, warp - 2, lane, abort);
     }

@@ -623,7 +623,9 @@ def fp4_tile_scales(scales):
 
 def fp4_untile_scales(tiles, rows, blocks):
     """The inverse of fp4_tile_scales: bytes [rows, blocks]."""
-    rt, ct, _ = tiles.shape
+    rt, ct = -(-rows // 128), -(-blocks // 4)
+    if tuple(tiles.shape) != (rt, ct, 512):
+        raise ValueError(f"tiles must have shape {(rt, ct, 512)}, got {tuple(tiles.shape)}")
     return tiles.view(rt, ct, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(rt * 128, ct * 4)[:rows, :blocks]
 
 

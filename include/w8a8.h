@@ -374,7 +374,9 @@ W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format
  *   has codes and x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and
  *   without that copy the call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M
  *   and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,
- *   else W8A8_ERR_WORKSPACE; may be NULL on the BF16 path.  path_taken as for w8a8_linear. */
+ *   else W8A8_ERR_WORKSPACE; may be NULL on the BF16 path.  Calls that may be in flight at
+ *   once (two streams, two captured graphs) need workspaces of their own.  path_taken as for
+ *   w8a8_linear. */
 W8A8_API w8a8_status_t w8a8_fp4_linear(const w8a8_bf16_t *x, int64_t M, int64_t K,
                                        const w8a8_fp4_weight_t *w, const w8a8_bf16_t *bias,
                                        w8a8_bf16_t *y, void *workspace, size_t workspace_bytes,

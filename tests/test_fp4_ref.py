@@ -54,6 +54,9 @@ def test_scale_tiles_follow_the_formula(rows, blocks):
         assert t[r // 128, b // 4, 16 * (r % 32) + 4 * (r % 128 // 32) + b % 4] == s[r, b]
     assert torch.equal(w8.fp4_untile_scales(t, rows, blocks), s)
     assert int(t.count_nonzero()) == int(s.count_nonzero())         # zeros past the end
+    assert torch.equal(w8.fp4_tile_scales(s.view(torch.float8_e4m3fn)), t)
+    with pytest.raises(ValueError):
+        w8.fp4_untile_scales(t, rows + 128, blocks)
 
 
 def test_binding_refuses_before_the_library(monkeypatch):

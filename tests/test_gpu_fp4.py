@@ -10,6 +10,9 @@ to the running sum; a step's error is a few units of FP32 in the last place of t
 number involved, which the sum S of the magnitudes bounds: 2^-22 S a step, and 8 steps'
 worth for the join of split sums, the factors and the bias."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -145,10 +148,11 @@ def _check_product(y, xq, wq, bias, what):
 
 
 SHAPES = [(1, 32, 1), (1, 64, 130), (5, 96, 128), (16, 256, 256), (17, 288, 100), (31, 544, 257), (33, 1024, 129),
-          (64, 2048, 384), (65, 160, 40), (100, 4096, 200), (128, 512, 512), (3, 8192, 24)]
+          (64, 2048, 384), (65, 160, 40), (100, 4096, 200), (128, 512, 512), (3, 8192, 24), (3, 131104, 40),
+          (70, 262176, 9)]
 LARGE = [(129, 64, 8), (129, 32, 1), (256, 256, 256), (257, 288, 255), (300, 544, 520), (512, 1056, 1000),
          (1000, 2048, 777), (640, 4096, 2056), (2100, 320, 3000),
-         (1000, 16384, 8), (300, 8192, 1001), (70, 2048, 300), (19000, 96, 264)]
+         (1000, 16384, 8), (300, 8192, 1001), (70, 2048, 300), (19000, 96, 264), (2000, 70016, 264)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -367,6 +371,32 @@ def test_graph_capture_and_side_stream():
             static.copy_(x.roll(shift, 0))
             graph.replay()
             assert torch.equal(out.view(torch.int16), want.roll(shift, 0).view(torch.int16))
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first call of each kernel is captured: the graph replays the bits of
+    the eager calls that follow."""
+    code = """
+import torch, block_wise_w8a8_b200 as w8
+g = torch.Generator().manual_seed(1)
+x = [torch.randn((M, 1024), generator=g).bfloat16().cuda() for M in (2, 40, 700, 9000)]
+w = torch.randn((520, 1024), generator=g).bfloat16().cuda()
+torch.cuda.synchronize()
+def run():
+    wt = w8.FP4Weight(w)
+    return [w8.fp4_linear(a, wt) for a in x] + list(w8.block_norm(x[3], x[3])) + [w8.block_norm_fp4(x[3], x[3])[1].codes]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, run()))
+assert w8.device_error() == 0
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_c_abi_refusals():

@@ -488,6 +488,7 @@ def bf16_linear(x, w, bias=None, out=None):
 
 # ---- the microscaled 4-bit linear and the norms around a block -----------------------------
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+_FP4_FEW_ROWS = 4        # up to these w8a8_fp4_linear needs no workspace
 _FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 
 
@@ -507,25 +508,34 @@ def _fp4_tiles(rows, K, format):
     return (-(-rows // 128), -(-K // (4 * _FP4_BLOCK[format])), 512)
 
 
+_Tensor, _BF16, _U8 = torch.Tensor, torch.bfloat16, torch.uint8
+
+
 def _fits(t, shape, dtype, device):
     """Whether t is what _in accepts, in one expression: the small calls' common case."""
-    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+    return (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.device == device
             and t.is_contiguous())
+
+
+def _need_bf16(t, name):
+    """_need for BF16, in one expression where t is as it should be."""
+    if not (type(t) is _Tensor and t.dtype is _BF16 and t.is_cuda and t.is_contiguous()):
+        _need(t, _BF16, name)
 
 
 def _bf16_out(out, like, shape, device):
     """_out for a BF16 output; a new one is made from a tensor at hand, which takes less time."""
     if out is None:
-        return like.new_empty(shape, dtype=torch.bfloat16)
-    return _out(out, shape, torch.bfloat16, device, "out")
+        return like.new_empty(shape, dtype=_BF16)
+    return _out(out, shape, _BF16, device, "out")
 
 
 def _column(t, shape, device, name):
     """An optional BF16 input: checked, as its address (None where there is none)."""
     if t is None:
         return None
-    if not _fits(t, shape, torch.bfloat16, device):
-        _in(t, shape, torch.bfloat16, device, name)
+    if not _fits(t, shape, _BF16, device):
+        _in(t, shape, _BF16, device, name)
     return t.data_ptr()
 
 
@@ -539,13 +549,13 @@ class FP4Tensor:
 
     def __init__(self, codes, scales, factor, format):
         fmt = _fp4_format(format)
-        _need(codes, torch.uint8, "codes")
+        _need(codes, _U8, "codes")
         rows, half = codes.shape
         dev, tiles = codes.device, _fp4_tiles(rows, 2 * half, format)
         _fp4_k(2 * half)
         self.rows, self.K, self.format, self.device = rows, 2 * half, format, dev
-        if not _fits(scales, tiles, torch.uint8, dev):
-            _in(scales, tiles, torch.uint8, dev, "scales")
+        if not _fits(scales, tiles, _U8, dev):
+            _in(scales, tiles, _U8, dev, "scales")
         if fmt:
             if not _fits(factor, (rows,), torch.float32, dev):
                 _in(factor, (rows,), torch.float32, dev, "factor")
@@ -593,7 +603,7 @@ def _fp4_empty(rows, K, format, device):
     at = (rows * K // 2 + 255) // 256 * 256
     end = at + rt * ct * 512
     nv = format == "nvfp4"
-    q._buffer = torch.empty(end + 4 * rows if nv else end, dtype=torch.uint8, device=device)
+    q._buffer = torch.empty(end + 4 * rows if nv else end, dtype=_U8, device=device)
     base = q._buffer.data_ptr()
     q._ptrs = (base, base + at, base + end if nv else None)
     return q
@@ -616,8 +626,8 @@ def fp4_tile_scales(scales):
         raise ValueError("scales must be a matrix of bytes")
     R, C = scales.shape
     rt, ct = -(-R // 128), -(-C // 4)
-    full = torch.zeros((rt * 128, ct * 4), dtype=torch.uint8, device=scales.device)
-    full[:R, :C] = scales.contiguous().view(torch.uint8)
+    full = torch.zeros((rt * 128, ct * 4), dtype=_U8, device=scales.device)
+    full[:R, :C] = scales.contiguous().view(_U8)
     return full.view(rt, 4, 32, ct, 4).permute(0, 3, 2, 1, 4).reshape(rt, ct, 512).contiguous()
 
 
@@ -634,12 +644,12 @@ def fp4_quantize(x, format="nvfp4", out=None):
     power-of-two scale; "nvfp4": blocks of 16 with an E4M3 scale and a float32 factor per
     row.  A row's codes depend on that row alone."""
     fmt = _fp4_format(format)
-    _need(x, torch.bfloat16, "x")
+    _need_bf16(x, "x")
     rows, K = x.shape
     dev = x.device
     q = _fp4_out(out, rows, K, format, dev)
     _check("w8a8_fp4_quantize",
-           lib().w8a8_fp4_quantize(x.data_ptr(), rows, K, fmt, *q._ptrs, _stream(dev)))
+           (_lib or lib()).w8a8_fp4_quantize(x.data_ptr(), rows, K, fmt, *q._ptrs, _stream(dev)))
     return q
 
 
@@ -648,7 +658,7 @@ def fp4_dequantize(q, out=None):
     if not isinstance(q, FP4Tensor):
         raise TypeError("q must be an FP4Tensor")
     y = _bf16_out(out, q._any(), (q.rows, q.K), q.device)
-    _check("w8a8_fp4_dequantize", lib().w8a8_fp4_dequantize(
+    _check("w8a8_fp4_dequantize", (_lib or lib()).w8a8_fp4_dequantize(
         *q._ptrs, q.rows, q.K, FP4_FORMATS[q.format], y.data_ptr(), _stream(q.device)))
     return y
 
@@ -664,10 +674,10 @@ class FP4Weight:
                 raise TypeError("q must be an FP4Tensor")
             self.N, self.K, self.device, format = q.rows, q.K, q.device, q.format
             if w_bf16 is not None:
-                _in(w_bf16, (q.rows, q.K), torch.bfloat16, q.device, "w")
+                _in(w_bf16, (q.rows, q.K), _BF16, q.device, "w")
         else:
             _fp4_format(format)
-            _need(w_bf16, torch.bfloat16, "w")
+            _need(w_bf16, _BF16, "w")
             (self.N, self.K), self.device = w_bf16.shape, w_bf16.device
             if self.K and self.K % 32 == 0:
                 q = fp4_quantize(w_bf16, format)
@@ -699,7 +709,7 @@ def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False
     """y = x W^T + bias in BF16 with x quantized to the weight's 4-bit format in the call.
     x: [..., K] BF16 (leading dimensions flattened), any number of rows and outputs.  K not a
     multiple of 32 takes the BF16 GEMM on the weight's BF16 copy."""
-    _need(x, torch.bfloat16, "x")
+    _need_bf16(x, "x")
     K = x.shape[-1]
     M = math.prod(x.shape[:-1])
     dev = x.device
@@ -707,15 +717,17 @@ def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False
     b = _column(bias, (weight.N,), dev, "bias")
     shape = (*x.shape[:-1], weight.N)
     out = _bf16_out(out, x, shape, dev)
+    size = 0
     if workspace is None:
-        size = int(lib().w8a8_fp4_linear_workspace_bytes(M, K, FP4_FORMATS[weight.format]))
+        if M > _FP4_FEW_ROWS:
+            size = lib().w8a8_fp4_linear_workspace_bytes(M, K, FP4_FORMATS[weight.format])
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(size, dtype=_U8, device=dev)
     else:
         size = workspace.numel()
-        _out(workspace, (size,), torch.uint8, dev, "workspace")
+        _out(workspace, (size,), _U8, dev, "workspace")
     path = ctypes.c_int(-1) if return_path else None
-    _check("w8a8_fp4_linear", lib().w8a8_fp4_linear(
+    _check("w8a8_fp4_linear", (_lib or lib()).w8a8_fp4_linear(
         x.data_ptr(), M, K, weight._rec, b, out.data_ptr(), workspace.data_ptr() if size else None, size,
         path, _stream(dev)))
     return (out, path.value) if return_path else out
@@ -730,19 +742,19 @@ def fp4_linear_prequant(q, weight, bias=None, out=None):
         raise ValueError(f"weight is {weight.format}, the activations {q.format}")
     b = _column(bias, (weight.N,), q.device, "bias")
     out = _bf16_out(out, q._any(), (q.rows, weight.N), q.device)
-    _check("w8a8_fp4_linear_prequant", lib().w8a8_fp4_linear_prequant(
+    _check("w8a8_fp4_linear_prequant", (_lib or lib()).w8a8_fp4_linear_prequant(
         *q._ptrs, q.rows, q.K, weight._rec, b, out.data_ptr(), _stream(q.device)))
     return out
 
 
 def _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, res_scale, eps, h_out):
     """Checks shared by both forms -> (h_out, the C call's arguments up to K)."""
-    _need(h, torch.bfloat16, "h")
+    _need_bf16(h, "h")
     shape = h.shape
     M, K = shape
     dev = h.device
-    if not _fits(y, shape, torch.bfloat16, dev):
-        _in(y, shape, torch.bfloat16, dev, "y")
+    if not _fits(y, shape, _BF16, dev):
+        _in(y, shape, _BF16, dev, "y")
     if post_gamma is not None and not post_norm:
         raise ValueError("post_gamma needs post_norm")
     rows = gate if gate is not None else scale if scale is not None else shift
@@ -752,7 +764,7 @@ def _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm,
     if h_out is None:
         h_out = torch.empty_like(h)
     else:
-        _out(h_out, shape, torch.bfloat16, dev, "h_out")
+        _out(h_out, shape, _BF16, dev, "h_out")
     return h_out, (h.data_ptr(), y.data_ptr(), int(post_norm), _column(post_gamma, (K,), dev, "post_gamma"),
                    _column(gate, (B, K), dev, "gate"), res_scale, _column(pre_gamma, (K,), dev, "pre_gamma"),
                    _column(scale, (B, K), dev, "scale"), _column(shift, (B, K), dev, "shift"), max(M // B, 1),
@@ -768,9 +780,9 @@ def block_norm(h, y, post_gamma=None, gate=None, pre_gamma=None, scale=None, shi
     be None.  h_out may be h (in place) -> (h', n)."""
     h_out, args = _block_norm_args(h, y, post_gamma, gate, pre_gamma, scale, shift, post_norm, res_scale, eps,
                                    h_out)
-    n = torch.empty_like(h) if n_out is None else _out(n_out, h.shape, torch.bfloat16, h.device, "n_out")
+    n = torch.empty_like(h) if n_out is None else _out(n_out, h.shape, _BF16, h.device, "n_out")
     _check("w8a8_block_norm",
-           lib().w8a8_block_norm(*args, h_out.data_ptr(), n.data_ptr(), _stream(h.device)))
+           (_lib or lib()).w8a8_block_norm(*args, h_out.data_ptr(), n.data_ptr(), _stream(h.device)))
     return h_out, n
 
 
@@ -783,7 +795,7 @@ def block_norm_fp4(h, y, format="nvfp4", post_gamma=None, gate=None, pre_gamma=N
                                    h_out)
     q = _fp4_out(out, *h.shape, format, h.device)
     _check("w8a8_block_norm_fp4",
-           lib().w8a8_block_norm_fp4(*args, fmt, h_out.data_ptr(), *q._ptrs, _stream(h.device)))
+           (_lib or lib()).w8a8_block_norm_fp4(*args, fmt, h_out.data_ptr(), *q._ptrs, _stream(h.device)))
     return h_out, q
 
 

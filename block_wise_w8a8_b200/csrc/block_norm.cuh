@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
     const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2;
     const int S = p.stages;
     StreamTail<W> &sm = *reinterpret_cast<StreamTail<W> *>(ring + static_cast<size_t>(S) * 2 * row_bytes);
-    asm volatile("griddepcontrol.launch_dependents;");
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const int np = static_cast<int>(p.K / 8);
@@ -198,6 +197,9 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             mbar_init(&sm.full[s], 1);
         sm.abort = 0;
         fence_barrier_init();
+    }
+    fp4::wait_for_previous();
+    if (threadIdx.x == 0) {
         int64_t r = blockIdx.x;
         for (int s = 0; s < S && r < p.M; ++s, r += gridDim.x)
             fetch(r, s);
@@ -229,6 +231,8 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
                 }
             }
         }
+        if (r + gridDim.x >= p.M)
+            fp4::let_next_start();
         // A wait that gives up is recorded; the row is then worked on as it is, so that every
         // warp reaches every barrier.
         mbar_wait(&sm.full[s], phase, abort);
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
 {
     __shared__ __align__(16) float s_red[2][W];
     __shared__ __align__(16) uint32_t s_top[W];
-    asm volatile("griddepcontrol.launch_dependents;");
+    fp4::wait_for_previous();
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const int64_t r = blockIdx.x;
@@ -389,6 +393,7 @@ __global__ void __launch_bounds__(W * 32) row_kernel(const Params p)
     }
     rstd = rstd_of(row_sum<W>(acc.x + acc.y, s_red[1], warp, lane), inv_k, p.eps);
 
+    fp4::let_next_start();
     // n, and for kNv its largest magnitude; a long row's n is formed again for its codes
     uint32_t top = 0, m[P] = {};
     for (int at_c = 0; at_c < (kLong && kOut == fp4::kMx ? 0 : np); at_c += kChunk) {

@@ -598,8 +598,8 @@ template <int kFmt, int BT>
 constexpr size_t kSkinnySmemBytes = sizeof(SkinnySmem<kFmt, BT>) + 1024;
 constexpr int kQuantRows = 4;            // most rows of kQuant
 
-// kQuant, kNv: the row factors, from the rows' largest magnitudes over all of K.  Runs before
-// the CTA's set-up is complete, so that its loads overlap it; four warps.
+// kQuant, kNv: the row factors, from the rows' largest magnitudes over all of K.  Four warps,
+// before the CTA's set-up is complete, so that the loads overlap it.
 template <class S>
 __device__ __forceinline__ void row_tops(S &sm, const GemmParams &p, const uint16_t *x, int tid, uint32_t lane)
 {
@@ -728,13 +728,16 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         tmem_alloc(&sm.tmem_base, kCols);
         tmem_relinquish();
     }
+    if (kQuant)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     if (kQuant && kFmt == kNv && warp >= 2)
         row_tops(sm, p, x, static_cast<int>(threadIdx.x) - 64, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!kQuant)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
         uint32_t it = 0;

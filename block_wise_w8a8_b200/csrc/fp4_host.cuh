@@ -37,13 +37,37 @@ w8a8_status_t fp4_shape(int64_t rows, int64_t K)
     return W8A8_OK;
 }
 
+// Every kernel of this file is launched as a programmatic dependent: its set-up overlaps the
+// end of whatever precedes it on the stream, and it reads and writes nothing before that has
+// completed (griddepcontrol.wait).  A chain of small kernels saves about 1 us at each.
+template <class... Params, class... Args>
+w8a8_status_t launch_dependent(void (*kern)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                               int cluster, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
 // ------------------------------------------------------------------ quantizer
 // One row a CTA of W warps, P pieces of 8 values a lane.
 template <int kFmt, int W, int P>
 w8a8_status_t launch_fp4_rows(const fp4::QParams &p, cudaStream_t stream)
 {
-    fp4::quantize_kernel<kFmt, W, P><<<static_cast<unsigned>(p.rows_pad), W * 32, 0, stream>>>(p);
-    return launch_status();
+    return launch_dependent(fp4::quantize_kernel<kFmt, W, P>, p.rows_pad, W * 32, 0, stream, 1, p);
 }
 
 // As many CTAs as fit, each with a ring of rows.
@@ -67,8 +91,7 @@ w8a8_status_t launch_fp4_stream(const fp4::QParams &p, int dev, cudaStream_t str
         }
     }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(g_dev[dev].sms) * kResident);
-    kern<<<static_cast<unsigned>(grid), W * 32, smem, stream>>>(p, stages);
-    return launch_status();
+    return launch_dependent(kern, grid, W * 32, smem, stream, 1, p, stages);
 }
 
 // The ring from 2 rows a resident CTA on, where a lane has up to 32 values; a row on its own
@@ -118,8 +141,6 @@ w8a8_status_t launch_fp4_quantize(const uint16_t *x, int64_t rows, int64_t K, in
 }
 
 // ------------------------------------------------------------------ product
-// Products are launched as programmatic dependents: their set-up overlaps the end of whatever
-// precedes them on the stream, and they read nothing before that has completed.
 w8a8_status_t fp4_maps(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int format,
                        uint32_t box_rows, CUtensorMap &mc, CUtensorMap &ms)
 {
@@ -154,19 +175,6 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
     auto kern = fp4::gemm_pair_kernel<kFmt, kTma>;
     constexpr size_t smem = fp4::kPairSmemBytes<kFmt, kTma>;
     static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(fp4::PairEpi<kTma>::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     int pairs;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -177,7 +185,17 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
             if (e != cudaSuccess)
                 return cuda_fail(e);
             int n = 0;
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
             cfg.gridDim = dim3(static_cast<unsigned>(g_dev[dev].sms / 2 * 2));
+            cfg.blockDim = dim3(fp4::PairEpi<kTma>::kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
                 cudaGetLastError();
                 n = g_dev[dev].sms / 2;
@@ -192,10 +210,8 @@ w8a8_status_t launch_fp4_pair(const Fp4Operand &x, const Fp4Operand &w, fp4::Gem
         p.num_full = tiles - tail;
         p.num_units = tiles + tail;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, p.num_units)));
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, my, p);
-    return e == cudaSuccess ? launch_status() : cuda_fail(e);
+    return launch_dependent(kern, 2 * std::min(pairs, p.num_units), fp4::PairEpi<kTma>::kThreads, smem, stream, 2, mx, mw,
+                            mxs, mws, my, p);
 }
 
 // xb: BF16 activations to quantize on the way (kQuant), else null.
@@ -236,22 +252,7 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
     int splits = 1;
     while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].sms && p.slices >= splits * 2 * (splits < 4 ? 4 : 8))
         splits *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(fp4::kSkinnyThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = kQuant ? 1 : 2;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, xb, p);
-    return e == cudaSuccess ? launch_status() : cuda_fail(e);
+    return launch_dependent(kern, tiles * splits, fp4::kSkinnyThreads, smem, stream, splits, mx, mw, mxs, mws, xb, p);
 }
 
 template <int kFmt>
@@ -327,8 +328,7 @@ template <int kOut, int W, int P, bool kLong>
 w8a8_status_t launch_norm_rows(const bnorm::Params &p, cudaStream_t stream)
 {
     const int64_t grid = kOut == bnorm::kOutBf16 ? p.M : p.M_pad;
-    bnorm::row_kernel<kOut, W, P, kLong><<<static_cast<unsigned>(grid), W * 32, 0, stream>>>(p);
-    return launch_status();
+    return launch_dependent(bnorm::row_kernel<kOut, W, P, kLong>, grid, W * 32, 0, stream, 1, p);
 }
 
 // As many CTAs as fit, each with a ring of `stages` rows.
@@ -352,8 +352,7 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
         }
     }
     const int64_t grid = std::min<int64_t>(p.M, static_cast<int64_t>(g_dev[dev].sms) * kResident);
-    kern<<<static_cast<unsigned>(grid), W * 32, smem, stream>>>(p);
-    return launch_status();
+    return launch_dependent(kern, grid, W * 32, smem, stream, 1, p);
 }
 
 // The ring from 4 rows a resident CTA on.  There a lane has 16 values (32 in the longest

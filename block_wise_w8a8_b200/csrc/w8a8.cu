@@ -1065,9 +1065,8 @@ w8a8_status_t w8a8_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, c
     const int64_t grid = (rows * ((K + run - 1) / run) + fp4::kWarps - 1) / fp4::kWarps;
     if (grid > 0x7FFFFFFF)
         return W8A8_ERR_SHAPE;
-    auto kern = format == W8A8_FP4_MX ? fp4::dequantize_kernel<fp4::kMx> : fp4::dequantize_kernel<fp4::kNv>;
-    kern<<<static_cast<unsigned>(grid), fp4::kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launch_status();
+    return launch_dependent(format == W8A8_FP4_MX ? fp4::dequantize_kernel<fp4::kMx> : fp4::dequantize_kernel<fp4::kNv>,
+                            grid, fp4::kWarps * 32, 0, static_cast<cudaStream_t>(stream), 1, p);
 }
 
 size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format)

@@ -160,12 +160,14 @@ __device__ __forceinline__ void normalise(const Pre &c, float rstd, const uint32
 }
 
 // ------------------------------------------------------------------ many rows
+constexpr int kMaxRing = 16;             // rows of a ring at most
+
 // Shared memory: the ring, `stages` slots of h and y of a row (4 K bytes), then this.
 template <int W>
 struct StreamTail {
     alignas(16) float red[2][2][W];      // by row parity and sum
     alignas(16) uint32_t top[2][W];
-    uint64_t full[fp4::kMaxRing];
+    uint64_t full[kMaxRing];
     int abort;
 };
 

@@ -376,21 +376,24 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // is paid half as often as with 8.  Up to kStreamPieces of them, K <= 1024 W.
 constexpr int kStreamPieces = 2;
 constexpr int kStreamWarps = 32;                 // warps a SM
-constexpr int kMaxRing = 16;                     // rows of a ring at most
+// Two rows a CTA hide the copies: 16384 x 4096 nvfp4 30.4 us with 2, 32.4 with 6 and more,
+// mxfp4 29.5 and 30.5 (64 to 1024 values a row: alike); the reads of a deeper ring only crowd
+// the writes.
+constexpr int kRing = 2;
 template <int W>
 struct StreamTail {                              // behind the ring
     alignas(16) uint32_t top[2][W];              // by row parity
-    uint64_t full[kMaxRing];
+    uint64_t full[kRing];
     int abort;
 };
 
 template <int kFmt, int W>
-__global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kernel(const QParams p, const int stages)
+__global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kernel(const QParams p)
 {
     constexpr int P = kStreamPieces;
     extern __shared__ __align__(128) uint8_t ring[];
     const uint32_t row_bytes = static_cast<uint32_t>(p.K) * 2;
-    StreamTail<W> &sm = *reinterpret_cast<StreamTail<W> *>(ring + static_cast<size_t>(stages) * row_bytes);
+    StreamTail<W> &sm = *reinterpret_cast<StreamTail<W> *>(ring + kRing * row_bytes);
     const int warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
     const int np = static_cast<int>(p.K / 16);
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
         bulk_load(ring + static_cast<size_t>(s) * row_bytes, p.x + r * p.K, row_bytes, &sm.full[s]);
     };
     if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s)
+        for (int s = 0; s < kRing; ++s)
             mbar_init(&sm.full[s], 1);
         sm.abort = 0;
         fence_barrier_init();
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
     wait_for_previous();
     if (threadIdx.x == 0) {
         int64_t r = blockIdx.x;
-        for (int s = 0; s < stages && r < p.rows; ++s, r += gridDim.x)
+        for (int s = 0; s < kRing && r < p.rows; ++s, r += gridDim.x)
             fetch(r, s);
     }
     __syncthreads();
@@ -462,8 +465,8 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
         if (W == 1)
             __syncwarp();
         // every thread has read the slot
-        if (threadIdx.x == 0 && r + static_cast<int64_t>(stages) * gridDim.x < p.rows)
-            fetch(r + static_cast<int64_t>(stages) * gridDim.x, s);
+        if (threadIdx.x == 0 && r + static_cast<int64_t>(kRing) * gridDim.x < p.rows)
+            fetch(r + static_cast<int64_t>(kRing) * gridDim.x, s);
         uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
             if (stores && b < np_pad)
                 scales[scale_at + i * (kStep / kTileBlocks * 512)] = static_cast<uint8_t>(u.byte);
         }
-        if (++s == stages) {
+        if (++s == kRing) {
             s = 0;
             phase ^= 1;
         }

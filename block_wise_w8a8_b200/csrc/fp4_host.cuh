@@ -70,28 +70,28 @@ w8a8_status_t launch_fp4_rows(const fp4::QParams &p, cudaStream_t stream)
     return launch_dependent(fp4::quantize_kernel<kFmt, W, P>, p.rows_pad, W * 32, 0, stream, 1, p);
 }
 
-// As many CTAs as fit, each with a ring of rows.
+// As many CTAs as fit, each with a ring of rows (2 K kRing bytes, 64 KB at most of 16 warps'
+// share of 111) and, used or not, all of its share of the SM: see launch_norm_stream.
 template <int kFmt, int W>
 w8a8_status_t launch_fp4_stream(const fp4::QParams &p, int dev, cudaStream_t stream)
 {
     constexpr int kResident = fp4::kStreamWarps / W;
     const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(fp4::StreamTail<W>);
-    const int stages = static_cast<int>(std::min<size_t>(fp4::kMaxRing, budget / (2 * static_cast<size_t>(p.K))));
-    const size_t smem = static_cast<size_t>(stages) * 2 * p.K + sizeof(fp4::StreamTail<W>);
+    const size_t smem = budget + sizeof(fp4::StreamTail<W>);
     auto kern = fp4::quantize_stream_kernel<kFmt, W>;
     constexpr int slot = kFmt * 5 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : 4);
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!g_dev[dev].fp4_stream_attr_set[slot]) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(budget + sizeof(fp4::StreamTail<W>)));
+                                                       static_cast<int>(smem));
             if (e != cudaSuccess)
                 return cuda_fail(e);
             g_dev[dev].fp4_stream_attr_set[slot] = true;
         }
     }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(g_dev[dev].sms) * kResident);
-    return launch_dependent(kern, grid, W * 32, smem, stream, 1, p, stages);
+    return launch_dependent(kern, grid, W * 32, smem, stream, 1, p);
 }
 
 // The ring from 2 rows a resident CTA on, where a lane has up to 32 values; a row on its own
@@ -337,15 +337,23 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
 {
     constexpr int kResident = P > 2 ? 1 : bnorm::kStreamWarps / W;    // CTAs a SM
     const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(bnorm::StreamTail<W>);
-    p.stages = static_cast<int32_t>(std::min<size_t>(fp4::kMaxRing, budget / (4 * static_cast<size_t>(p.K))));
-    const size_t smem = static_cast<size_t>(p.stages) * 4 * p.K + sizeof(bnorm::StreamTail<W>);
+    // About 64 KB of rows in flight on a SM, at least two rows a CTA (three where it is alone):
+    // 32768 x 4096 169 us with 2 rows of 16 KB on each of two CTAs, 188 with 3, 191 with 6 (as
+    // much is written as read, and the reads of a deeper ring crowd the writes); 8192 x 8192,
+    // one CTA, 93 us with 2 rows, 88 with 3, 89 with 6.
+    const size_t row = 4 * static_cast<size_t>(p.K), want = (64 * 1024 / kResident + row / 2) / row;
+    p.stages = static_cast<int32_t>(
+        std::min<size_t>({bnorm::kMaxRing, budget / row, std::max<size_t>(want, kResident == 1 ? 3 : 2)}));
+    // all of a CTA's share of the SM, used or not: with less, more CTAs fit on some SMs than the
+    // grid has for each (32768 x 1536 nvfp4: 98 us for 87)
+    const size_t smem = budget + sizeof(bnorm::StreamTail<W>);
     auto kern = bnorm::stream_kernel<kOut, W, P>;
     constexpr int slot = (kOut + 1) * 6 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : P == 2 ? 4 : 5);
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!g_dev[dev].norm_stream_attr_set[slot]) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(budget + sizeof(bnorm::StreamTail<W>)));
+                                                       static_cast<int>(smem));
             if (e != cudaSuccess)
                 return cuda_fail(e);
             g_dev[dev].norm_stream_attr_set[slot] = true;

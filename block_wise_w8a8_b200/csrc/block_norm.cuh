@@ -106,7 +106,8 @@ __device__ __forceinline__ void add_squares(const uint32_t (&w)[4], float2 &acc)
     }
 }
 
-// Sum (or maximum) over the W warps of a row through s[W]; every thread of the row takes part.
+// Sum over the W warps of a row through s[kSlots<W>] (zeros behind W); every thread of the row
+// takes part.
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float *s, int warp, uint32_t lane)
 {
@@ -165,8 +166,9 @@ constexpr int kMaxRing = 16;             // rows of a ring at most
 // Shared memory: the ring, `stages` slots of h and y of a row (4 K bytes), then this.
 template <int W>
 struct StreamTail {
-    alignas(16) float red[2][2][W];      // by row parity and sum
-    alignas(16) uint32_t top[2][W];
+    static constexpr int kSlots = fp4::kSlots<W>;
+    alignas(16) float red[2][2][kSlots]; // by row parity and sum
+    alignas(16) uint32_t top[2][kSlots];
     uint64_t full[kMaxRing];
     int abort;
 };
@@ -197,6 +199,9 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s)
             mbar_init(&sm.full[s], 1);
+        for (int i = W; i < fp4::kSlots<W>; ++i)
+            for (int par = 0; par < 2; ++par)
+                sm.red[par][0][i] = sm.red[par][1][i] = 0.0f, sm.top[par][i] = 0;
         sm.abort = 0;
         fence_barrier_init();
     }

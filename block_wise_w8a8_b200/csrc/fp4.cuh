@@ -246,8 +246,12 @@ __device__ __forceinline__ int pieces_padded(int64_t KT)
     return static_cast<int>(KT) * 4 * kBlockLanes<kFmt>;
 }
 
-// Largest magnitude pattern over the W warps of a row (s[W], if W > 1 in shared memory); every
-// thread of the row takes part.
+// Places for a value of each of W warps, read by fours from 3 on.
+template <int W>
+constexpr int kSlots = W < 3 ? W : (W + 3) / 4 * 4;
+
+// Largest magnitude pattern over the W warps of a row (s[kSlots<W>], zeros behind W, if W > 1
+// in shared memory); every thread of the row takes part.
 template <int W>
 __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *s, int warp, uint32_t lane)
 {
@@ -382,7 +386,7 @@ constexpr int kStreamWarps = 32;                 // warps a SM
 constexpr int kRing = 2;
 template <int W>
 struct StreamTail {                              // behind the ring
-    alignas(16) uint32_t top[2][W];              // by row parity
+    alignas(16) uint32_t top[2][kSlots<W>];      // by row parity
     uint64_t full[kRing];
     int abort;
 };
@@ -416,6 +420,8 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRing; ++s)
             mbar_init(&sm.full[s], 1);
+        for (int i = W; i < kSlots<W>; ++i)
+            sm.top[0][i] = sm.top[1][i] = 0;
         sm.abort = 0;
         fence_barrier_init();
     }

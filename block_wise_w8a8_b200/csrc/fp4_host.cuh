@@ -79,37 +79,55 @@ w8a8_status_t launch_fp4_stream(const fp4::QParams &p, int dev, cudaStream_t str
     const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(fp4::StreamTail<W>);
     const size_t smem = budget + sizeof(fp4::StreamTail<W>);
     auto kern = fp4::quantize_stream_kernel<kFmt, W>;
-    constexpr int slot = kFmt * 5 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : 4);
+    bool &attr_set = g_dev[dev].fp4_stream_attr_set[kFmt][W];
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_dev[dev].fp4_stream_attr_set[slot]) {
+        if (!attr_set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        static_cast<int>(smem));
             if (e != cudaSuccess)
                 return cuda_fail(e);
-            g_dev[dev].fp4_stream_attr_set[slot] = true;
+            attr_set = true;
         }
     }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(g_dev[dev].sms) * kResident);
     return launch_dependent(kern, grid, W * 32, smem, stream, 1, p);
 }
 
-// The ring from 2 rows a resident CTA on, where a lane has up to 32 values; a row on its own
-// is split over as many warps as it fills with 8 values a lane, up to 16.
+// The ring from 2 rows a resident CTA on, where a lane has up to 32 values, with about as many
+// warps as that takes (8192 x 10240 nvfp4: 38.4 us with 10, 42.9 with 16; 16384 x 5120: 39.1
+// with 5, 41.8 with 8; 3, 6 and 7 gain nothing over 4 and 8).  A row on its own is split over
+// as many warps as it fills with 8 values a lane, up to 16.
 template <int kFmt>
 w8a8_status_t launch_fp4_quantize_t(const fp4::QParams &p, int dev, cudaStream_t stream)
 {
     const int64_t k = p.K, per_warp = 2 * g_dev[dev].sms * fp4::kStreamWarps;
-    if (k <= 1024 && p.rows >= per_warp)
-        return launch_fp4_stream<kFmt, 1>(p, dev, stream);
-    if (k > 1024 && k <= 2048 && p.rows >= per_warp / 2)
-        return launch_fp4_stream<kFmt, 2>(p, dev, stream);
-    if (k > 2048 && k <= 4096 && p.rows >= per_warp / 4)
-        return launch_fp4_stream<kFmt, 4>(p, dev, stream);
-    if (k > 4096 && k <= 8192 && p.rows >= per_warp / 8)
-        return launch_fp4_stream<kFmt, 8>(p, dev, stream);
-    if (k > 8192 && k <= 16384 && p.rows >= per_warp / 16)
-        return launch_fp4_stream<kFmt, 16>(p, dev, stream);
+    const int64_t warps = (k + 1023) / 1024;
+    if (warps <= 16 && p.rows >= per_warp / warps) {
+        switch (warps) {
+        case 1:
+            return launch_fp4_stream<kFmt, 1>(p, dev, stream);
+        case 2:
+            return launch_fp4_stream<kFmt, 2>(p, dev, stream);
+        case 3:
+        case 4:
+            return launch_fp4_stream<kFmt, 4>(p, dev, stream);
+        case 5:
+            return launch_fp4_stream<kFmt, 5>(p, dev, stream);
+        case 6:
+        case 7:
+        case 8:
+            return launch_fp4_stream<kFmt, 8>(p, dev, stream);
+        case 9:
+        case 10:
+            return launch_fp4_stream<kFmt, 10>(p, dev, stream);
+        case 11:
+        case 12:
+            return launch_fp4_stream<kFmt, 12>(p, dev, stream);
+        default:
+            return launch_fp4_stream<kFmt, 16>(p, dev, stream);
+        }
+    }
     if (k <= 256)
         return launch_fp4_rows<kFmt, 1, 1>(p, stream);
     if (k <= 512)
@@ -348,15 +366,15 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
     // grid has for each (32768 x 1536 nvfp4: 98 us for 87)
     const size_t smem = budget + sizeof(bnorm::StreamTail<W>);
     auto kern = bnorm::stream_kernel<kOut, W, P>;
-    constexpr int slot = (kOut + 1) * 6 + (W == 1 ? 0 : W == 2 ? 1 : W == 4 ? 2 : W == 8 ? 3 : P == 2 ? 4 : 5);
+    bool &attr_set = g_dev[dev].norm_stream_attr_set[kOut + 1][P > 2 ? 17 : W];
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_dev[dev].norm_stream_attr_set[slot]) {
+        if (!attr_set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        static_cast<int>(smem));
             if (e != cudaSuccess)
                 return cuda_fail(e);
-            g_dev[dev].norm_stream_attr_set[slot] = true;
+            attr_set = true;
         }
     }
     const int64_t grid = std::min<int64_t>(p.M, static_cast<int64_t>(g_dev[dev].sms) * kResident);
@@ -364,26 +382,50 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
 }
 
 // The ring from 4 rows a resident CTA on.  There a lane has 16 values (32 in the longest
-// rows), which spreads a row's reductions over enough of them; a row on its own is split
-// over as many warps as it fills.
+// rows), which spreads a row's reductions over enough of them, and a row as many warps as
+// that takes, for idle ones are places that another row could have: 32768 x 2560 nvfp4 126 us
+// with 5 warps, 176 with 8 (bf16 109, 125), 32768 x 1280 75 us with 3, 84 with 4, 16384 x 6144
+// 177 us with 12, 196 with 16; 14 for 16 loses (16384 x 7168: 208 us, 201).  A row on its own
+// is split over as many warps as it fills.
 template <int kOut>
 w8a8_status_t launch_block_norm(const bnorm::Params &p, cudaStream_t stream)
 {
     int dev;
     W8A8_TRY(current_device(dev));
     const int64_t k = p.K, per_warp = 4 * g_dev[dev].sms * bnorm::kStreamWarps;
-    if (k <= 512 && p.M >= per_warp)
-        return launch_norm_stream<kOut, 1, 2>(p, dev, stream);
-    if (k > 512 && k <= 1024 && p.M >= per_warp / 2)
-        return launch_norm_stream<kOut, 2, 2>(p, dev, stream);
-    if (k > 1024 && k <= 2048 && p.M >= per_warp / 4)
-        return launch_norm_stream<kOut, 4, 2>(p, dev, stream);
-    if (k > 2048 && k <= 4096 && p.M >= per_warp / 8)
-        return launch_norm_stream<kOut, 8, 2>(p, dev, stream);
-    if (k > 4096 && k <= 8192 && p.M >= per_warp / 16)
-        return launch_norm_stream<kOut, 16, 2>(p, dev, stream);
-    if (k > 8192 && k <= 16384 && p.M >= per_warp / 16)
-        return launch_norm_stream<kOut, 16, 4>(p, dev, stream);
+    const int64_t warps = (k + 511) / 512;
+    if (warps <= 32 && p.M >= per_warp / std::min<int64_t>(warps, 16)) {
+        switch (warps) {
+        case 1:
+            return launch_norm_stream<kOut, 1, 2>(p, dev, stream);
+        case 2:
+            return launch_norm_stream<kOut, 2, 2>(p, dev, stream);
+        case 3:
+            return launch_norm_stream<kOut, 3, 2>(p, dev, stream);
+        case 4:
+            return launch_norm_stream<kOut, 4, 2>(p, dev, stream);
+        case 5:
+            return launch_norm_stream<kOut, 5, 2>(p, dev, stream);
+        case 6:
+            return launch_norm_stream<kOut, 6, 2>(p, dev, stream);
+        case 7:
+        case 8:
+            return launch_norm_stream<kOut, 8, 2>(p, dev, stream);
+        case 9:
+        case 10:
+            return launch_norm_stream<kOut, 10, 2>(p, dev, stream);
+        case 11:
+        case 12:
+            return launch_norm_stream<kOut, 12, 2>(p, dev, stream);
+        case 13:
+        case 14:
+        case 15:
+        case 16:
+            return launch_norm_stream<kOut, 16, 2>(p, dev, stream);
+        default:
+            return launch_norm_stream<kOut, 16, 4>(p, dev, stream);
+        }
+    }
     if (k <= 256)
         return launch_norm_rows<kOut, 1, 1, false>(p, stream);
     if (k <= 512)

@@ -67,6 +67,24 @@ def test_all_factors(M, K, B):
     assert bool((big[M] == 5).all()) and bool((nb[M] == 5).all())
 
 
+# rows whose length takes a number of warps that is no power of two
+@pytest.mark.parametrize("M,K,B", [(3200, 1288, 4), (3300, 1536, 1), (2000, 2080, 5), (1900, 2560, 1900), (1600, 2880, 2),
+                                   (1000, 4128, 8), (999, 5120, 1), (800, 6144, 4)])
+def test_lengths_between_powers_of_two(M, K, B):
+    t = _inputs(M, K, B, M + K)
+    h2, n = w8.block_norm(**t, res_scale=0.75, eps=1e-5)
+    _check(t, h2, n, K, 0.75, True, 1e-5)
+    if K % 32:
+        return
+    for fmt in ("mxfp4", "nvfp4"):
+        want = w8.fp4_quantize(n, fmt)
+        h4, q = w8.block_norm_fp4(t["h"], t["y"], fmt, **{k: v for k, v in t.items() if k not in "hy"}, res_scale=0.75,
+                                  eps=1e-5)
+        assert _same(h4, h2)
+        assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+        assert q.factor is None or torch.equal(q.factor, want.factor)
+
+
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("gammas", [True, False])
 @pytest.mark.parametrize("mod", [True, False])

@@ -86,6 +86,22 @@ def test_quantize_bit_exact(fmt, M, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", [(9500, 992), (4800, 1504), (2500, 2560), (2400, 4096), (1900, 5120), (1600, 6144),
+                                 (1200, 8192), (950, 10240), (790, 12256), (640, 16384)])
+def test_quantize_many_rows(fmt, M, K):
+    """Several rows a CTA: the first 41 against the plain form, the others their repetitions."""
+    part = _rows(41, K, M + K)
+    x = part.repeat(-(-M // 41), 1)[:M].contiguous()
+    q, few = w8.fp4_quantize(x.cuda(), fmt), w8.fp4_quantize(part.cuda(), fmt)
+    _check_quantized(few, part, f"{fmt} 41x{K}")
+    again = torch.arange(M, device="cuda") % 41
+    assert torch.equal(q.codes, few.codes[again])
+    assert torch.equal(ref.plain_scales(q), ref.plain_scales(few)[again])
+    if q.factor is not None:
+        assert torch.equal(q.factor.view(torch.int32), few.factor.view(torch.int32)[again])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_quantize_ties_and_near_ties(fmt):
     """Every BF16 significand against every other, over the binades that a block can hold:
     the rounding boundaries of codes and scales and their neighbours."""

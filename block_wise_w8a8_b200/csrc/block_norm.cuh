@@ -19,7 +19,8 @@
 //                  h and y copied into a ring in shared memory (one bulk copy each) while they
 //                  work.  A lane has the same columns in every row: for P <= 2 their factors
 //                  stay in registers and are read again when the rows' group b changes; for
-//                  P = 4 they come from L1 or L2 where they are used.
+//                  more they come from L1 or L2 for each row, ahead of the wait for the row and
+//                  of the second sum (4096 x 16384 nvfp4: 165 us; where they are used, 219).
 //   row_kernel     few rows, or rows too long for the ring: one row a W warps, straight from
 //                  global memory; longer rows are read again for each pass (kLong).
 #pragma once
@@ -63,38 +64,54 @@ struct Post {
 struct Pre {
     float2 pre[4], shift[4];
 };
-__device__ __forceinline__ void load_factor(const uint16_t *p, float none, float2 (&f)[4])
+// The same as they are read: pairs of BF16.
+struct RawPost {
+    uint4 gamma, gate;
+};
+struct RawPre {
+    uint4 gamma, scale, shift;
+};
+__device__ __forceinline__ uint4 raw_factor(const uint16_t *p, int64_t at, uint32_t none)
 {
-    if (p != nullptr) {
-        uint32_t w[4];
-        unpack4(__ldg(reinterpret_cast<const uint4 *>(p)), w);
+    return p != nullptr ? __ldg(reinterpret_cast<const uint4 *>(p + at)) : make_uint4(none, none, none, none);
+}
+constexpr uint32_t kOnes = 0x3F803F80u;
+__device__ __forceinline__ RawPost fetch_post(const Params &p, int64_t col, int64_t mod)
+{
+    return {raw_factor(p.post_gamma, col, kOnes), raw_factor(p.gate, mod + col, kOnes)};
+}
+__device__ __forceinline__ RawPre fetch_pre(const Params &p, int64_t col, int64_t mod)
+{
+    return {raw_factor(p.pre_gamma, col, kOnes), raw_factor(p.scale, mod + col, 0), raw_factor(p.shift, mod + col, 0)};
+}
+__device__ __forceinline__ void make_post(const RawPost &raw, Post &c)
+{
+    uint32_t gamma[4], gate[4];
+    unpack4(raw.gamma, gamma);
+    unpack4(raw.gate, gate);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = pair_of(w[i]);
-    } else {
+    for (int i = 0; i < 4; ++i)
+        c.post[i] = __fmul2_rn(pair_of(gamma[i]), pair_of(gate[i]));
+}
+__device__ __forceinline__ void make_pre(const RawPre &raw, Pre &c)
+{
+    uint32_t gamma[4], scale[4], shift[4];
+    unpack4(raw.gamma, gamma);
+    unpack4(raw.scale, scale);
+    unpack4(raw.shift, shift);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = make_float2(none, none);
+    for (int i = 0; i < 4; ++i) {
+        c.pre[i] = __fmul2_rn(pair_of(gamma[i]), __fadd2_rn(make_float2(1.0f, 1.0f), pair_of(scale[i])));
+        c.shift[i] = pair_of(shift[i]);
     }
 }
 __device__ __forceinline__ void load_post(const Params &p, int64_t col, int64_t mod, Post &c)
 {
-    float2 gate[4];
-    load_factor(p.post_gamma == nullptr ? nullptr : p.post_gamma + col, 1.0f, c.post);
-    load_factor(p.gate == nullptr ? nullptr : p.gate + mod + col, 1.0f, gate);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c.post[i] = __fmul2_rn(c.post[i], gate[i]);
+    make_post(fetch_post(p, col, mod), c);
 }
 __device__ __forceinline__ void load_pre(const Params &p, int64_t col, int64_t mod, Pre &c)
 {
-    float2 scale[4];
-    load_factor(p.pre_gamma == nullptr ? nullptr : p.pre_gamma + col, 1.0f, c.pre);
-    load_factor(p.scale == nullptr ? nullptr : p.scale + mod + col, 0.0f, scale);
-    load_factor(p.shift == nullptr ? nullptr : p.shift + mod + col, 0.0f, c.shift);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c.pre[i] = __fmul2_rn(c.pre[i], __fadd2_rn(make_float2(1.0f, 1.0f), scale[i]));
+    make_pre(fetch_pre(p, col, mod), c);
 }
 
 __device__ __forceinline__ void add_squares(const uint32_t (&w)[4], float2 &acc)
@@ -238,6 +255,13 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
                 }
             }
         }
+        RawPost raw_post[kKeep ? 1 : P];
+        if (!kKeep) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (b0 + i * kStep < np)
+                    raw_post[kKeep ? 0 : i] = fetch_post(p, (b0 + i * kStep) * 8, mod);
+        }
         if (r + gridDim.x >= p.M)
             fp4::let_next_start();
         // A wait that gives up is recorded; the row is then worked on as it is, so that every
@@ -271,11 +295,18 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             if (b < np) {
                 Post &f = post[kKeep ? i : 0];
                 if (!kKeep)
-                    load_post(p, b * 8, mod, f);
+                    make_post(raw_post[kKeep ? 0 : i], f);
                 update(f, p.res_scale, rstd, h[i], y[i]);
                 *reinterpret_cast<uint4 *>(h_row + b * 8) = pack4(y[i]);
                 add_squares(y[i], acc);
             }
+        }
+        RawPre raw_pre[kKeep ? 1 : P];
+        if (!kKeep) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (b0 + i * kStep < np)
+                    raw_pre[kKeep ? 0 : i] = fetch_pre(p, (b0 + i * kStep) * 8, mod);
         }
         if (W == 1)
             __syncwarp();
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             if (b < np) {
                 Pre &f = pre[kKeep ? i : 0];
                 if (!kKeep)
-                    load_pre(p, b * 8, mod, f);
+                    make_pre(raw_pre[kKeep ? 0 : i], f);
                 normalise(f, rstd, y[i], h[i]);
                 if constexpr (kOut == kOutBf16)
                     *reinterpret_cast<uint4 *>(p.n_out + r * p.K + b * 8) = pack4(h[i]);

@@ -355,23 +355,26 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
 {
     constexpr int kResident = P > 2 ? 1 : bnorm::kStreamWarps / W;    // CTAs a SM
     const size_t budget = 226 * 1024 / kResident - 1024 - sizeof(bnorm::StreamTail<W>);
-    // About 64 KB of rows in flight on a SM, at least two rows a CTA (three where it is alone):
-    // 32768 x 4096 169 us with 2 rows of 16 KB on each of two CTAs, 188 with 3, 191 with 6 (as
-    // much is written as read, and the reads of a deeper ring crowd the writes); 8192 x 8192,
-    // one CTA, 93 us with 2 rows, 88 with 3, 89 with 6.
+    // About 64 KB of rows in flight on a SM, at least two rows a CTA (three where it is alone
+    // and its rows are no longer than that): 32768 x 4096 169 us with 2 rows of 16 KB on each of
+    // two CTAs, 188 with 3, 191 with 6 (as much is written as read, and the reads of a deeper
+    // ring crowd the writes); 8192 x 8192, one CTA, 93 us with 2 rows, 88 with 3, 89 with 6.
     const size_t row = 4 * static_cast<size_t>(p.K), want = (64 * 1024 / kResident + row / 2) / row;
     p.stages = static_cast<int32_t>(
-        std::min<size_t>({bnorm::kMaxRing, budget / row, std::max<size_t>(want, kResident == 1 ? 3 : 2)}));
-    // all of a CTA's share of the SM, used or not: with less, more CTAs fit on some SMs than the
-    // grid has for each (32768 x 1536 nvfp4: 98 us for 87)
-    const size_t smem = budget + sizeof(bnorm::StreamTail<W>);
+        std::min<size_t>({bnorm::kMaxRing, budget / row, std::max<size_t>(want, kResident == 1 && P <= 2 ? 3 : 2)}));
+    // P <= 2: all of a CTA's share of the SM, used or not, for with less more CTAs fit on some
+    // SMs than the grid has for each (32768 x 1536 nvfp4: 98 us for 87).  P > 2: the factors are
+    // read again for each row, and what the ring leaves is L1 that they stay in (4096 x 16384:
+    // 108 us, 123 with the whole share).
+    const size_t most = budget + sizeof(bnorm::StreamTail<W>);
+    const size_t smem = P > 2 ? p.stages * row + sizeof(bnorm::StreamTail<W>) : most;
     auto kern = bnorm::stream_kernel<kOut, W, P>;
-    bool &attr_set = g_dev[dev].norm_stream_attr_set[kOut + 1][P > 2 ? 17 : W];
+    bool &attr_set = g_dev[dev].norm_stream_attr_set[kOut + 1][P > 2 ? 14 + P : W];
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!attr_set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(smem));
+                                                       static_cast<int>(most));
             if (e != cudaSuccess)
                 return cuda_fail(e);
             attr_set = true;
@@ -381,12 +384,13 @@ w8a8_status_t launch_norm_stream(bnorm::Params p, int dev, cudaStream_t stream)
     return launch_dependent(kern, grid, W * 32, smem, stream, 1, p);
 }
 
-// The ring from 4 rows a resident CTA on.  There a lane has 16 values (32 in the longest
-// rows), which spreads a row's reductions over enough of them, and a row as many warps as
-// that takes, for idle ones are places that another row could have: 32768 x 2560 nvfp4 126 us
-// with 5 warps, 176 with 8 (bf16 109, 125), 32768 x 1280 75 us with 3, 84 with 4, 16384 x 6144
-// 177 us with 12, 196 with 16; 14 for 16 loses (16384 x 7168: 208 us, 201).  A row on its own
-// is split over as many warps as it fills.
+// The ring from 4 rows a resident CTA on.  There a lane has 16 values (24 or 32 in rows of
+// more than 8192: 8192 x 12288 nvfp4 206 us with 24, 273 with 32), which spreads a row's
+// reductions over enough of them, and a row as many warps as that takes, for idle ones are
+// places that another row could have: 32768 x 2560 nvfp4 126 us with 5 warps, 176 with 8 (bf16
+// 109, 125), 32768 x 1280 75 us with 3, 84 with 4, 16384 x 6144 177 us with 12, 196 with 16; 14
+// for 16 loses (16384 x 7168: 208 us, 201).  A row on its own is split over as many warps as it
+// fills.
 template <int kOut>
 w8a8_status_t launch_block_norm(const bnorm::Params &p, cudaStream_t stream)
 {
@@ -422,6 +426,15 @@ w8a8_status_t launch_block_norm(const bnorm::Params &p, cudaStream_t stream)
         case 15:
         case 16:
             return launch_norm_stream<kOut, 16, 2>(p, dev, stream);
+        case 17:
+        case 18:
+        case 19:
+        case 20:
+        case 21:
+        case 22:
+        case 23:
+        case 24:
+            return launch_norm_stream<kOut, 16, 3>(p, dev, stream);
         default:
             return launch_norm_stream<kOut, 16, 4>(p, dev, stream);
         }

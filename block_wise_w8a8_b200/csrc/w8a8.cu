@@ -36,7 +36,7 @@ struct DeviceInfo {
     bool norm_attr_set[4] = {false, false, false, false};
     int norm_max_clusters[norm::kMaxCluster + 1] = {};    // by cluster size, 0 = unknown
     int fp4_pairs[4] = {};                                 // by format and store: pairs that fit, 0 = unknown
-    bool norm_stream_attr_set[3][18] = {};                 // bnorm::stream_kernel by output and warps (17: the longest rows)
+    bool norm_stream_attr_set[3][19] = {};                 // bnorm::stream_kernel by output and warps (17, 18: 3, 4 pieces)
     bool fp4_stream_attr_set[2][17] = {};                  // fp4::quantize_stream_kernel by format and warps
     bool fp4_skinny_attr_set[10] = {};                     // by format and token tile, quantizing or not
 };

@@ -69,7 +69,8 @@ def test_all_factors(M, K, B):
 
 # rows whose length takes a number of warps that is no power of two
 @pytest.mark.parametrize("M,K,B", [(3200, 1288, 4), (3300, 1536, 1), (2000, 2080, 5), (1900, 2560, 1900), (1600, 2880, 2),
-                                   (1000, 4128, 8), (999, 5120, 1), (800, 6144, 4)])
+                                   (1000, 4128, 8), (999, 5120, 1), (800, 6144, 4), (620, 12288, 5), (620, 12320, 4),
+                                   (600, 16384, 600)])
 def test_lengths_between_powers_of_two(M, K, B):
     t = _inputs(M, K, B, M + K)
     h2, n = w8.block_norm(**t, res_scale=0.75, eps=1e-5)

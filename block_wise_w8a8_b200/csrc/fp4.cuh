@@ -34,6 +34,8 @@
 // block % 4.  Rows and blocks past the end of the matrix have scale 0.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace w8a8 {

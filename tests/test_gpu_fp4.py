@@ -347,6 +347,37 @@ def test_guard_takes_bf16(M, K, N):
     assert torch.equal(y.view(torch.int16), w8.bf16_linear(x, w, b).view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 512), (5, 2048, 4096), (200, 1024, 1000)])
+def test_weight_written_just_before_its_product(fmt, M, K, N):
+    """The weight quantized again in place between products, eager and replayed: every product
+    sees the codes of the call before it."""
+    g = _gen(M + N)
+    x = torch.randn((M, K), generator=g).bfloat16().cuda()
+    ws = [torch.randn((N, K), generator=g).bfloat16().cuda() for _ in range(3)]
+    want = [w8.fp4_linear(x, w8.FP4Weight(w, fmt)) for w in ws]
+    q = w8.fp4_quantize(ws[0], fmt)
+    wt = w8.FP4Weight(q=q)
+
+    def run():
+        out = []
+        for w in ws * 4:
+            w8.fp4_quantize(w, fmt, out=q)
+            out.append(w8.fp4_linear(x, wt))
+        return out
+    torch.cuda.synchronize()
+    for got in (run(), run()):
+        assert all(torch.equal(a, b) for a, b in zip(got, want * 4))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want * 4))
+        for y in got:
+            y.zero_()
+
+
 def test_empty():
     wt = w8.FP4Weight(torch.randn((8, 64), generator=_gen(1)).bfloat16().cuda())
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")

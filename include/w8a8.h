@@ -315,8 +315,9 @@ W8A8_API w8a8_status_t w8a8_rowwise_linear(const int8_t *xq, const float *xs, in
  *                A = max(max|row|, 2^-100), factor = fl32(A / 2688),
  *                s = e4m3(448 max|block| / A), code = e2m1(2688 v / (s A)), 0 where s = 0.
  *   e2m1 and e4m3 round to nearest even and saturate; the quotients are rounded as if
- *   exact.  A value that rounds to zero has code 0 or 8 (-0).  A value is code * scale (* factor).  Infinities and NaN: the block's scale is
- *   NaN (MX), the row's factor is NaN (NV), their codes 0.
+ *   exact.  A value that rounds to zero has code 0 or 8 (-0).  A value is code * scale
+ *   (* factor).  Infinities and NaN: the block's scale is NaN (MX), the row's factor is NaN
+ *   (NV), their codes 0.
  *
  * Layout of a quantized matrix [rows, K], K a positive multiple of 32 up to 2^24:
  *   codes  [rows, K/2] bytes, element 2 i in the low half of byte i;

@@ -266,9 +266,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
         }
         if (r + gridDim.x >= p.M)
             fp4::let_next_start();
-        // A wait that gives up is recorded; the row is then worked on as it is, so that every
-        // warp reaches every barrier.
-        mbar_wait(&sm.full[s], phase, abort);
+        mbar_wait(&sm.full[s], phase, abort);        // how a ring ends: fp4::hold_ring
         const uint8_t *slot = ring + static_cast<size_t>(s) * 2 * row_bytes;
         uint32_t y[P][4], h[P][4];
 #pragma unroll
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
             __syncwarp();
         rstd = rstd_of(row_sum<W>(acc.x + acc.y, sm.red[par][1], warp, lane), inv_k, p.eps);
         // every thread has read the slot
-        if (threadIdx.x == 0 && r + static_cast<int64_t>(S) * gridDim.x < p.M)
+        if (threadIdx.x == 0 && r + static_cast<int64_t>(S) * gridDim.x < p.M && !*abort)
             fetch(r + static_cast<int64_t>(S) * gridDim.x, s);
         uint32_t top = 0, m[P] = {};
 #pragma unroll
@@ -352,6 +350,8 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
     }
     if constexpr (kOut != kOutBf16)
         fp4::zero_scales(p.scales, p.M, p.M_pad, KT, blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0 && *abort)
+        fp4::hold_ring();
 }
 
 // ------------------------------------------------------------------ few or long rows

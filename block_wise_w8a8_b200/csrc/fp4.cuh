@@ -393,6 +393,19 @@ struct StreamTail {                              // behind the ring
     int abort;
 };
 
+// How a ring ends when a wait for a row gives up: the flag goes up in front of a block barrier,
+// and behind it thread 0, finding it up, fills no slot again, for the copy into this one may
+// still be in flight and its barrier's phase open.  The rows from there on are worked on as
+// they are, so that every warp reaches every barrier; their waits give up at once.  Last,
+// thread 0 holds the CTA's shared memory, which may be another CTA's next, until the copies in
+// flight have landed: they need microseconds, it waits a millisecond.
+__device__ __forceinline__ void hold_ring()
+{
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull)
+        ;
+}
+
 template <int kFmt, int W>
 __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kernel(const QParams p)
 {
@@ -439,8 +452,6 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, par ^= 1) {
         if (r + gridDim.x >= p.rows)
             let_next_start();
-        // A wait that gives up is recorded; the row is then coded as it is, so that every warp
-        // reaches every barrier.
         mbar_wait(&sm.full[s], phase, abort);
         const uint8_t *slot = ring + static_cast<size_t>(s) * row_bytes;
         uint32_t w[P][2][4], m[P];
@@ -473,7 +484,7 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
         if (W == 1)
             __syncwarp();
         // every thread has read the slot
-        if (threadIdx.x == 0 && r + static_cast<int64_t>(kRing) * gridDim.x < p.rows)
+        if (threadIdx.x == 0 && r + static_cast<int64_t>(kRing) * gridDim.x < p.rows && !*abort)
             fetch(r + static_cast<int64_t>(kRing) * gridDim.x, s);
         uint8_t *codes = p.codes + r * (p.K / 2), *scales = p.scales + scale_row(r, KT);
 #pragma unroll
@@ -497,6 +508,8 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
         }
     }
     zero_scales(p.scales, p.rows, p.rows_pad, KT, blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0 && *abort)
+        hold_ring();
 }
 
 // y [rows, K] BF16 = the values the codes stand for: fl(code * scale) is exact, the product

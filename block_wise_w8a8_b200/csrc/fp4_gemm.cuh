@@ -14,6 +14,8 @@
 // partial tile are zeros in memory.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gemm.cuh"
@@ -103,6 +105,32 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
     else
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
+}
+
+// v xf wf + bias for a sum v and its row's and column's factors (kNv), rounded at the product of
+// the factors and at the result.  The quantizer's factors lie between 2^-112 and 2^117, so their
+// product may leave FP32's normal range where the result does not (rows of 2^-90 times a weight
+// of 2^-30), and a zero sum would meet an infinity.  v then takes one factor after the other.
+// Both are above 1 or both below 2^-14 at such a place, and |v| is 0 or at least 2^-20: v wf
+// overflows, or loses bits, only where the result does.  A warp tests the range of its factors
+// once (products of few tokens +1% in time, many 0 to 2%; tested at each output 10 to 40%); an
+// output depends on its own v and factors alone.
+__device__ __forceinline__ bool normal_range(float p)
+{
+    return fabsf(p) >= 1.17549435e-38f && fabsf(p) <= 3.40282347e38f;
+}
+__device__ __forceinline__ float scaled(float v, float xf, float wf, float bias)
+{
+    const float p = xf * wf;
+    return normal_range(p) ? fmaf(v, p, bias) : fmaf(v * wf, xf, bias);
+}
+// Whether every product of one of the warp's factors a with one of its factors b is in the
+// normal range (false where one is negative or NaN).
+__device__ __forceinline__ bool normal_products(uint32_t a_min, uint32_t a_max, uint32_t b_min, uint32_t b_max)
+{
+    const float lo = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, a_min)) * __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, b_min));
+    const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, a_max), bm = __reduce_max_sync(0xFFFFFFFFu, b_max);
+    return max(am, bm) < 0x7F800000u && normal_range(lo) && normal_range(__uint_as_float(am) * __uint_as_float(bm));
 }
 
 // One lane of the converged warp.  The tcgen05 and TMA instructions below are issued under
@@ -463,14 +491,20 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
             constexpr int kSteps = E::kWidth / E::kChunk;
             const int steps = kTma && cut >= 0 ? kSteps / 2 : kSteps;
             __syncwarp();
+            const float xf = kFmt == kNv && m < p.M ? __ldg(p.xf + m) : 1.0f;
+            uint32_t wf_min = 0x3F800000u, wf_max = wf_min;
 #pragma unroll
             for (int j = 0; j < E::kWidth / 32; ++j) {
                 const int64_t n = n0 + j * 32 + lane;
-                wf[j * 32 + lane] = kFmt == kNv && n < p.N ? __ldg(p.wf + n) : 1.0f;
+                const float f = kFmt == kNv && n < p.N ? __ldg(p.wf + n) : 1.0f;
+                wf[j * 32 + lane] = f;
+                wf_min = min(wf_min, __float_as_uint(f));
+                wf_max = max(wf_max, __float_as_uint(f));
                 bias[j * 32 + lane] =
                     p.bias != nullptr && n < p.N ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16) : 0.0f;
             }
-            const float xf = kFmt == kNv && m < p.M ? __ldg(p.xf + m) : 1.0f;
+            const bool all_plain =
+                kFmt != kNv || normal_products(__float_as_uint(xf), __float_as_uint(xf), wf_min, wf_max);
             __syncwarp();
             const uint32_t buf = i & 1;
             if (!gemm::gemm_wait(&sm.tfull[buf], (i >> 1) & 1, abort))
@@ -483,7 +517,7 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
             // free, and with the rest the accumulator.
             static_assert(2 * pair_sf_cols(kFmt) <= 96, "shared columns");
             const bool holds_shared = E::kParts == 1 || part != static_cast<int>(buf);
-            auto store_chunk = [&](const Chunk &r, int c0) {
+            auto store_chunk = [&](auto plain, const Chunk &r, int c0) {
                 if (kTma && lane == 0)
                     gemm::tma_store_wait_read();
                 __syncwarp();
@@ -496,8 +530,12 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                         const float2 f = *reinterpret_cast<const float2 *>(wf + c0 + e);
                         const float2 b = *reinterpret_cast<const float2 *>(bias + c0 + e);
                         const float v0 = __uint_as_float(r[e >> 5][e & 31]), v1 = __uint_as_float(r[e >> 5][(e & 31) + 1]);
-                        o[q] = kFmt == kNv ? pack_bf16x2(fmaf(v0, xf * f.x, b.x), fmaf(v1, xf * f.y, b.y))
-                                           : pack_bf16x2(v0 + b.x, v1 + b.y);
+                        if (kFmt != kNv)
+                            o[q] = pack_bf16x2(v0 + b.x, v1 + b.y);
+                        else if (decltype(plain)::value)
+                            o[q] = pack_bf16x2(fmaf(v0, xf * f.x, b.x), fmaf(v1, xf * f.y, b.y));
+                        else
+                            o[q] = pack_bf16x2(scaled(v0, xf, f.x, b.x), scaled(v1, xf, f.y, b.y));
                     }
                     st_shared_v4(out + (kTma ? lane * 128 + ((g ^ (lane & 7)) << 4) : gemm::stage_off(lane, g)),
                                  make_uint4(o[0], o[1], o[2], o[3]));
@@ -519,45 +557,51 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                 if (here && lane == 0)
                     arrive_remote(bar);
             };
-            if constexpr (kTma) {
-                Chunk r0, r1;
-                load_chunk(acc + column(0), r0);
-                load_chunk(acc + column(1), r1);
-                wait_chunk(r0);
-                wait_chunk(r1);
-                tc_fence_before();
-                __syncwarp();
-                arrive(true, shared);
-                arrive(steps == 2, drained + buf * 8);
-                store_chunk(r0, column(0));
-                if (steps == 4)
-                    load_chunk(acc + column(2), r0);
-                store_chunk(r1, column(1));
-                if (steps == 4) {
-                    load_chunk(acc + column(3), r1);
+            auto store_unit = [&](auto plain) {
+                if constexpr (kTma) {
+                    Chunk r0, r1;
+                    load_chunk(acc + column(0), r0);
+                    load_chunk(acc + column(1), r1);
                     wait_chunk(r0);
                     wait_chunk(r1);
                     tc_fence_before();
                     __syncwarp();
-                    arrive(true, drained + buf * 8);
-                    store_chunk(r0, column(2));
-                    store_chunk(r1, column(3));
-                }
-            } else {
-#pragma unroll 1
-                for (int step = 0; step < 4; ++step) {
-                    const int c0 = column(step);
-                    Chunk r;
-                    load_chunk(acc + c0, r);
-                    wait_chunk(r);
-                    if ((step == 2 && holds_shared) || step == 3) {
+                    arrive(true, shared);
+                    arrive(steps == 2, drained + buf * 8);
+                    store_chunk(plain, r0, column(0));
+                    if (steps == 4)
+                        load_chunk(acc + column(2), r0);
+                    store_chunk(plain, r1, column(1));
+                    if (steps == 4) {
+                        load_chunk(acc + column(3), r1);
+                        wait_chunk(r0);
+                        wait_chunk(r1);
                         tc_fence_before();
                         __syncwarp();
-                        arrive(true, step == 3 ? drained + buf * 8 : shared);
+                        arrive(true, drained + buf * 8);
+                        store_chunk(plain, r0, column(2));
+                        store_chunk(plain, r1, column(3));
                     }
-                    store_chunk(r, c0);
+                } else {
+#pragma unroll 1
+                    for (int step = 0; step < 4; ++step) {
+                        const int c0 = column(step);
+                        Chunk r;
+                        load_chunk(acc + c0, r);
+                        wait_chunk(r);
+                        if ((step == 2 && holds_shared) || step == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            arrive(true, step == 3 ? drained + buf * 8 : shared);
+                        }
+                        store_chunk(plain, r, c0);
+                    }
                 }
-            }
+            };
+            if (all_plain)
+                store_unit(std::true_type{});
+            else if constexpr (kFmt == kNv)
+                store_unit(std::false_type{});
         }
         if (kTma && lane == 0)
             gemm::tma_store_wait_all();
@@ -838,16 +882,28 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         if (p.bias != nullptr)
             bias = __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16);
     }
-    auto finish = [&](float v, int t) {
+    // the products of the warp's rows' factors with all of the tokens'
+    uint32_t xf_min = 0x3F800000u, xf_max = xf_min;
+    if (kFmt == kNv && warp >= 2)
+        for (int t = static_cast<int>(lane); t < tokens; t += 32) {
+            const uint32_t f = __float_as_uint(kQuant ? sm.factor[t] : __ldg(p.xf + m0 + t));
+            xf_min = min(xf_min, f);
+            xf_max = max(xf_max, f);
+        }
+    const bool all_plain =
+        kFmt != kNv || warp < 2 || normal_products(xf_min, xf_max, __float_as_uint(wf), __float_as_uint(wf));
+    auto finish = [&](auto plain, float v, int t) {
         const int64_t m = m0 + t;
-        if (kFmt == kNv)
-            v = fmaf(v, (kQuant ? sm.factor[t] : __ldg(p.xf + m)) * wf, bias);
-        else
+        const float xf = kFmt == kNv ? (kQuant ? sm.factor[t] : __ldg(p.xf + m)) : 1.0f;
+        if (kFmt != kNv)
             v = v + bias;
+        else if (decltype(plain)::value)
+            v = fmaf(v, xf * wf, bias);
+        else
+            v = scaled(v, xf, wf, bias);
         p.y[m * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
     };
-    if (warp >= 2 && gemm::gemm_wait(&sm.tfull, 0, abort)) {
-        tc_fence_after();
+    auto from_tmem = [&](auto plain) {
         const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
         for (int c = 0; c < tokens; c += 16) {
@@ -859,9 +915,16 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
                 if (splits > 1)
                     part[(c + i) * 128 + row] = __uint_as_float(v[i]);
                 else if (store && c + i < tokens)
-                    finish(__uint_as_float(v[i]), c + i);
+                    finish(plain, __uint_as_float(v[i]), c + i);
             }
         }
+    };
+    if (warp >= 2 && gemm::gemm_wait(&sm.tfull, 0, abort)) {
+        tc_fence_after();
+        if (splits > 1 || all_plain)
+            from_tmem(std::true_type{});
+        else if constexpr (kFmt == kNv)
+            from_tmem(std::false_type{});
     }
     tc_fence_before();
     __syncthreads();
@@ -870,7 +933,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         // tokens are dealt out to the ranks in equal runs
         const int each = (tokens + splits - 1) / splits;
         const int t1 = min(tokens, (rank + 1) * each);
-        if (store && !*abort) {
+        auto join = [&](auto plain) {
             // 8 tokens of 4 ranks in flight: a read of another SM's shared memory takes about
             // as long as one of L2
             for (int t0 = rank * each; t0 < t1; t0 += 8) {
@@ -898,8 +961,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (t0 + i < t1)
-                        finish(v[i], t0 + i);
+                        finish(plain, v[i], t0 + i);
             }
+        };
+        if (store && !*abort) {
+            if (all_plain)
+                join(std::true_type{});
+            else if constexpr (kFmt == kNv)
+                join(std::false_type{});
         }
         norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
     }

@@ -371,7 +371,8 @@ W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format
 /* Y[M, N] = X[M, K] W^T + bias with X quantized in the call to the weight's format:
  *     y[m,n] = bf16( factor_x[m] factor_w[n] * sum_k value_x[m,k] value_w[n,k] + bias[n] ),
  *   values without factors, FP32 accumulation, one rounding to BF16; the sum's order is fixed
- *   by M, N and K.  Guard: the 4-bit path runs iff K is a multiple of 32 up to 2^24, the weight
+ *   by M, N and K.  Factors whose product leaves FP32's normal range are applied one after the
+ *   other, so that only the result's own range counts.  Guard: the 4-bit path runs iff K is a multiple of 32 up to 2^24, the weight
  *   has codes and x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and
  *   without that copy the call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M
  *   and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,

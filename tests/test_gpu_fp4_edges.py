@@ -1,0 +1,108 @@
+"""The 4-bit linear at the ends of its ranges: row factors far from 1, weights without rows,
+the longest rows.
+
+Tolerance of a product as in the linear's own tests: half a BF16 step of the result (2^-8
+relative; 2^-134 where the result is subnormal in BF16), and for the FP32 accumulation and the
+factors 2^-22 a step of 64 products, and 8 steps more, of the sum of the magnitudes."""
+import pytest
+import torch
+
+import block_wise_w8a8_b200 as w8
+import fp4_ref as ref
+
+pytestmark = pytest.mark.gpu
+FORMATS = ("mxfp4", "nvfp4")
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert w8.device_error() == 0
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _nvfp4(rows, K, factor, seed, zero=False):
+    """An nvfp4 matrix with these row factors (a number or a row's each)."""
+    g = _gen(seed)
+    codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, generator=g) * (0 if zero else 1)
+    s = torch.randint(40, 100, (rows, K // 16), generator=g).to(torch.uint8)
+    f = torch.full((rows,), factor) if isinstance(factor, float) else factor
+    return w8.FP4Tensor(codes.to(torch.uint8).cuda(), w8.fp4_tile_scales(s).cuda(), f.float().cuda(), "nvfp4")
+
+
+def _check(y, x, w, bias):
+    xv, wv = ref.tensor_values(x), ref.tensor_values(w)
+    b = 0.0 if bias is None else bias.double()
+    want, size = xv @ wv.T + b, xv.abs() @ wv.abs().T + abs(b)
+    tol = want.abs() * 2.0 ** -8 + size * (x.K / 64 + 8) * 2.0 ** -22 + 2.0 ** -134
+    # a result that rounds past the largest BF16 number (2^128 - 2^119 from half a step above
+    # it on) is an infinity; within the tolerance of that border either is right
+    y, border = y.double(), 2.0 ** 128 - 2.0 ** 119
+    big = y.isinf() & (y.sign() == want.sign()) & (want.abs() + tol >= border)
+    bad = (~((y - want).abs() <= tol) & ~big).nonzero()
+    assert not len(bad), (f"{len(bad)} of {y.numel()} off, first {bad[0].tolist()}: {y[tuple(bad[0])].item()} "
+                          f"for {want[tuple(bad[0])].item()}")
+
+
+# few tokens (K split and not), pairs of CTAs with and without TMA stores, half tiles
+SHAPES = [(3, 512, 264), (3, 4096, 100), (40, 512, 264), (300, 512, 264), (300, 512, 263), (700, 96, 1000)]
+
+
+# exponents of x's and w's factors.  The quantizer's own lie between 2^-111.4 and 2^116.6.  The
+# products of the first five pairs leave FP32's normal range, the sums times both do not.
+@pytest.mark.parametrize("ex,ew", [(-101, -41), (-41, -101), (-111, -20), (-70, -70), (115, 2), (100, -100), (-111, 116), (116, -111),
+                                   (0, 0), (60, 50)])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_factors_far_from_one(M, K, N, ex, ew):
+    x, w = _nvfp4(M, K, 1.4 * 2.0 ** ex, 1), _nvfp4(N, K, 1.7 * 2.0 ** ew, 2)
+    wt = w8.FP4Weight(q=w)
+    bias = (torch.randn((N,), generator=_gen(3)) * 2.0 ** max(ex + ew, -120)).bfloat16().cuda()
+    for b in (None, bias):
+        _check(w8.fp4_linear_prequant(x, wt, b), x, w, b)
+
+
+@pytest.mark.parametrize("ex,ew", [(100, 60), (116, 116), (127, 1), (-111, -111)])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_a_zero_sum_is_the_bias(M, K, N, ex, ew):
+    """Whatever the factors, also where their product is no FP32 number."""
+    x, w = _nvfp4(M, K, 1.4 * 2.0 ** ex, 1, zero=True), _nvfp4(N, K, 1.7 * 2.0 ** ew, 2)
+    wt = w8.FP4Weight(q=w)
+    bias = torch.randn((N,), generator=_gen(3)).bfloat16().cuda()
+    assert bool((w8.fp4_linear_prequant(x, wt, bias) == bias).all())
+    assert bool((w8.fp4_linear_prequant(x, wt) == 0).all())
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_rows_of_every_size_in_one_tile(M, K, N):
+    """Factors of every size next to one another, NaN among them: each row and column is right,
+    and a row has the bits that it has among rows like itself."""
+    ex = torch.tensor([-111, -70, -20, 0, 20, 90])[torch.randint(0, 6, (M,), generator=_gen(4))].double()
+    ew = torch.tensor([-111, -60, -10, 0, 10, 30])[torch.randint(0, 6, (N,), generator=_gen(5))].double()
+    x, w = _nvfp4(M, K, 1.3 * torch.exp2(ex), 6), _nvfp4(N, K, 1.6 * torch.exp2(ew), 7)
+    y = w8.fp4_linear_prequant(x, w8.FP4Weight(q=w))
+    _check(y, x, w, None)
+    ones = x.factor.clone()
+    ones[ex != 0] = 1.3
+    like = w8.fp4_linear_prequant(w8.FP4Tensor(x.codes, x.scales, ones, "nvfp4"), w8.FP4Weight(q=w))
+    assert torch.equal(like[(ex == 0).cuda()].view(torch.int16), y[(ex == 0).cuda()].view(torch.int16))
+    bad = x.factor.clone()
+    bad[M // 2] = float("nan")
+    z = w8.fp4_linear_prequant(w8.FP4Tensor(x.codes, x.scales, bad, "nvfp4"), w8.FP4Weight(q=w))
+    rest = torch.arange(M) != M // 2
+    assert bool(z[M // 2].isnan().all()) and torch.equal(z[rest].view(torch.int16), y[rest].view(torch.int16))
+
+
+@pytest.mark.parametrize("ex,ew", [(-90, -30), (-30, -90), (100, -60), (100, 60)])
+@pytest.mark.parametrize("M", [1, 4, 20, 300])
+def test_linear_of_rows_far_from_one(M, ex, ew):
+    """The same from BF16 rows, quantized inside the product and before it; one row of zeros."""
+    K, N = 992, 264
+    x = (torch.randn((M, K), generator=_gen(M)) * 2.0 ** ex).bfloat16()
+    x[M - 1] = 0
+    w = w8.FP4Weight((torch.randn((N, K), generator=_gen(1)) * 2.0 ** ew).bfloat16().cuda(), keep_bf16=False)
+    y = w8.fp4_linear(x.cuda(), w)
+    _check(y, w8.fp4_quantize(x.cuda()), w.q, None)
+    assert bool((y[M - 1] == 0).all())

@@ -329,14 +329,15 @@ w8a8_status_t launch_fp4_linear_few(const uint16_t *x, int64_t M, int64_t K, con
                : launch_fp4_skinny<fp4::kNv, 16, true>(Fp4Operand{}, x, wo, p, stream);
 }
 
-// A weight record: consistent fields; the buffers are checked by whoever uses them.
+// A weight record: consistent fields; the buffers are checked by whoever uses them.  A weight
+// without rows has none (an empty tensor's address may be null).
 w8a8_status_t check_fp4_weight(const w8a8_fp4_weight_t *w, int64_t K)
 {
     if (w == nullptr || w->N < 0 || w->K != K || !fp4_format_ok(w->format))
         return W8A8_ERR_INVALID_ARG;
     if ((w->codes == nullptr) != (w->scales == nullptr))
         return W8A8_ERR_INVALID_ARG;
-    if (w->codes == nullptr && w->w_bf16 == nullptr && K > 0)
+    if (w->codes == nullptr && w->w_bf16 == nullptr && K > 0 && w->N > 0)
         return W8A8_ERR_INVALID_ARG;
     return W8A8_OK;
 }

@@ -1137,7 +1137,7 @@ w8a8_status_t w8a8_fp4_linear_prequant(const uint8_t *codes, const uint8_t *scal
                                        w8a8_bf16_t *y, void *stream)
 {
     W8A8_TRY(check_fp4_weight(w, K));
-    if (w->codes == nullptr)
+    if (w->codes == nullptr && w->N > 0)
         return W8A8_ERR_INVALID_ARG;
     W8A8_TRY(fp4_shape(M, K));
     W8A8_TRY(fp4_shape(w->N, K));

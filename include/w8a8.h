@@ -335,7 +335,8 @@ typedef enum {
 
 /* A weight [N, K] in 4 bits.  codes, scales, factor as above (factor NULL for MX); w_bf16:
  * [N, K] BF16, NULL if the caller keeps no copy for the guard's fallback.  codes and scales
- * may both be NULL if K is not a multiple of 32 (the layer then always takes BF16). */
+ * may both be NULL if K is not a multiple of 32 (the layer then always takes BF16); with
+ * N = 0 every buffer may be. */
 typedef struct {
     int64_t N;
     int64_t K;

@@ -106,3 +106,19 @@ def test_linear_of_rows_far_from_one(M, ex, ew):
     y = w8.fp4_linear(x.cuda(), w)
     _check(y, w8.fp4_quantize(x.cuda()), w.q, None)
     assert bool((y[M - 1] == 0).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [40, 64])
+def test_a_weight_without_rows(fmt, K):
+    w = torch.empty((0, K), dtype=torch.bfloat16, device="cuda")
+    for M in (0, 1, 7):
+        x = torch.randn((M, K), generator=_gen(M)).bfloat16().cuda()
+        y, path = w8.fp4_linear(x, w8.FP4Weight(w, fmt), return_path=True)
+        assert y.shape == (M, 0) and path == w8.PATH_NONE
+        if K == 64:
+            q = w8.fp4_quantize(w, fmt)
+            given = w8.FP4Tensor(q.codes, q.scales, q.factor, fmt)
+            for wt in (w8.FP4Weight(w, fmt, keep_bf16=False), w8.FP4Weight(q=q), w8.FP4Weight(q=given)):
+                assert w8.fp4_linear(x, wt).shape == (M, 0)
+                assert w8.fp4_linear_prequant(w8.fp4_quantize(x, fmt), wt).shape == (M, 0)

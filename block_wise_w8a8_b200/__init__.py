@@ -564,6 +564,14 @@ class FP4Tensor:
         self._buffer, self._parts = None, (codes, scales, factor)
         self._ptrs = (codes.data_ptr(), scales.data_ptr(), factor.data_ptr() if fmt else None)
 
+    # Copies are made from the tensors: the addresses are of those at hand.
+    def __copy__(self):
+        return FP4Tensor(*self._views(), self.format)
+
+    def __reduce__(self):
+        # clones: views of one buffer with two types cannot be saved
+        return FP4Tensor, (*(None if t is None else t.clone() for t in self._views()), self.format)
+
     def _any(self):
         return self._buffer if self._parts is None else self._parts[0]
 

@@ -4,6 +4,9 @@ the longest rows.
 Tolerance of a product as in the linear's own tests: half a BF16 step of the result (2^-8
 relative; 2^-134 where the result is subnormal in BF16), and for the FP32 accumulation and the
 factors 2^-22 a step of 64 products, and 8 steps more, of the sum of the magnitudes."""
+import copy
+import io
+
 import pytest
 import torch
 
@@ -122,3 +125,31 @@ def test_a_weight_without_rows(fmt, K):
             for wt in (w8.FP4Weight(w, fmt, keep_bf16=False), w8.FP4Weight(q=q), w8.FP4Weight(q=given)):
                 assert w8.fp4_linear(x, wt).shape == (M, 0)
                 assert w8.fp4_linear_prequant(w8.fp4_quantize(x, fmt), wt).shape == (M, 0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("given", [False, True])
+def test_copies_stand_for_their_own_tensors(fmt, given):
+    """A deep copy, and one from a file, keep their values when the first matrix is written
+    again or gone; a shallow copy is another name for it."""
+    def save(q):
+        f = io.BytesIO()
+        torch.save(q, f)
+        f.seek(0)
+        return torch.load(f, weights_only=False)
+    x, other = (torch.randn((130, 96), generator=_gen(s)).bfloat16().cuda() for s in (1, 2))
+    q = w8.fp4_quantize(x, fmt)
+    if given:
+        q = w8.FP4Tensor(q.codes.clone(), q.scales.clone(), None if q.factor is None else q.factor.clone(), fmt)
+    want = w8.fp4_dequantize(q)
+    deep, loaded, name = copy.deepcopy(q), save(q), copy.copy(q)
+    w8.fp4_quantize(other, fmt, out=q)
+    new = w8.fp4_dequantize(q)
+    assert not torch.equal(new, want)
+    del q
+    for c, y in ((deep, want), (loaded, want), (name, new)):
+        assert torch.equal(w8.fp4_dequantize(c), y)
+        code = ref.values(ref.unpack(c.codes), ref.plain_scales(c), c.factor, fmt)
+        assert torch.equal(code.float().bfloat16().double(), y.double())
+        w = w8.FP4Weight(q=c)
+        assert torch.equal(w8.fp4_linear_prequant(c, w), w8.fp4_linear_prequant(w8.fp4_quantize(x if y is want else other, fmt), w))

@@ -490,6 +490,7 @@ def bf16_linear(x, w, bias=None, out=None):
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 _FP4_FEW_ROWS = 4        # up to these w8a8_fp4_linear needs no workspace
 _FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+_FP4_MAX_K = 1 << 24     # longest row of the 4-bit operators
 
 
 def _fp4_format(format):
@@ -673,8 +674,9 @@ def fp4_dequantize(q, out=None):
 
 class FP4Weight:
     """A linear layer's weight in 4 bits: quantized from w_bf16 at construction, or given as
-    an FP4Tensor q.  w_bf16 is kept for the guard's BF16 path (K not a multiple of 32);
-    without it those shapes raise.  keep_bf16=False drops it after quantizing."""
+    an FP4Tensor q.  w_bf16 is kept for the guard's BF16 path (K not a multiple of 32, or above
+    2^24, which is not quantized; x not 16-byte aligned); without it those calls raise.
+    keep_bf16=False drops it after quantizing."""
 
     def __init__(self, w_bf16=None, format="nvfp4", q=None, keep_bf16=True):
         if q is not None:
@@ -687,7 +689,7 @@ class FP4Weight:
             _fp4_format(format)
             _need(w_bf16, _BF16, "w")
             (self.N, self.K), self.device = w_bf16.shape, w_bf16.device
-            if self.K and self.K % 32 == 0:
+            if self.K and self.K % 32 == 0 and self.K <= _FP4_MAX_K:
                 q = fp4_quantize(w_bf16, format)
                 if not keep_bf16:
                     w_bf16 = None
@@ -716,7 +718,8 @@ def fp4_linear_workspace_bytes(M, K, format="nvfp4"):
 def fp4_linear(x, weight, bias=None, out=None, workspace=None, return_path=False):
     """y = x W^T + bias in BF16 with x quantized to the weight's 4-bit format in the call.
     x: [..., K] BF16 (leading dimensions flattened), any number of rows and outputs.  K not a
-    multiple of 32 takes the BF16 GEMM on the weight's BF16 copy."""
+    multiple of 32, or above 2^24, takes the BF16 GEMM on the weight's BF16 copy, and so does
+    an x that is not 16-byte aligned."""
     _need_bf16(x, "x")
     K = x.shape[-1]
     M = math.prod(x.shape[:-1])

@@ -153,3 +153,19 @@ def test_copies_stand_for_their_own_tensors(fmt, given):
         assert torch.equal(code.float().bfloat16().double(), y.double())
         w = w8.FP4Weight(q=c)
         assert torch.equal(w8.fp4_linear_prequant(c, w), w8.fp4_linear_prequant(w8.fp4_quantize(x if y is want else other, fmt), w))
+
+
+def test_rows_longer_than_the_formats_take():
+    """The guard's BF16 path: no codes are made, and the results are the BF16 linear's."""
+    K = 2 ** 24 + 32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn((3, K), generator=g, device="cuda").bfloat16()
+    wt = w8.FP4Weight(w, keep_bf16=False)
+    assert wt.q is None and wt.w is w
+    for M in (2, 7):
+        x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+        y, path = w8.fp4_linear(x, wt, return_path=True)
+        assert path == w8.PATH_BF16 and torch.equal(y, w8.bf16_linear(x, w))
+    with pytest.raises(w8.W8A8Error) as e:
+        w8.fp4_quantize(w)
+    assert e.value.code == 2

@@ -54,6 +54,19 @@ def _check(y, x, w, bias):
 SHAPES = [(3, 512, 264), (3, 4096, 100), (40, 512, 264), (300, 512, 264), (300, 512, 263), (700, 96, 1000)]
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 16384, 30 * 128), (1, 16384, 31 * 128), (37, 16384, 36 * 128), (1, 4096, 66 * 128), (1, 4096, 67 * 128),
+                                   (20, 4096, 72 * 128), (3, 2048, 148 * 128), (3, 2048, 149 * 128), (768, 16384, 768), (1664, 37120, 1408),
+                                   (1664, 40960, 1536)])
+def test_sizes_around_the_limits_of_splitting(M, K, N):
+    """Numbers of tiles on both sides of those that clusters of 8, 4 and 2 take at once, and of
+    the one from which pairs of CTAs take long rows."""
+    x, w = _nvfp4(M, K, 1.4, 1), _nvfp4(N, K, 1.7, 2)
+    bias = torch.randn((N,), generator=_gen(3)).bfloat16().cuda()
+    y = w8.fp4_linear_prequant(x, w8.FP4Weight(q=w), bias)
+    _check(y, x, w, bias)
+    assert torch.equal(w8.fp4_linear_prequant(x, w8.FP4Weight(q=w), bias), y)
+
+
 # exponents of x's and w's factors.  The quantizer's own lie between 2^-111.4 and 2^116.6.  The
 # products of the first five pairs leave FP32's normal range, the sums times both do not.
 @pytest.mark.parametrize("ex,ew", [(-101, -41), (-41, -101), (-111, -20), (-70, -70), (115, 2), (100, -100), (-111, 116), (116, -111),

@@ -310,12 +310,16 @@ w8a8_status_t launch_fp4_gemm_t(const Fp4Operand &x, const Fp4Operand &w, const 
     if (p.M <= 64)
         return launch_fp4_skinny<kFmt, 64, false>(x, nullptr, w, p, stream);
     // From 65 tokens on pairs of CTAs, which do not split K, unless the output is so small and K
-    // so long that there are no more 128 x 128 tiles than slices of K: 1000 x 16384 x 8 20.1
-    // -> 10.0 us, 256 x 16384 x 4096 (64 tiles, 64 slices) 23.0 -> 20.2; on the other side
-    // 300 x 4096 x 1024 (24, 16) 8.9 us with pairs, 10.4 split, 2000 x 8192 x 512 (64, 32)
-    // 13.0 and 14.8.
+    // so long that there are no more 128 x 128 tiles than slices of K, and few enough tiles for
+    // the other kernel to split it: 1000 x 16384 x 8 20.1 -> 10.0 us, 256 x 16384 x 4096 (64
+    // tiles, 64 slices) 23.0 -> 20.2; on the other side 300 x 4096 x 1024 (24, 16) 8.9 us with
+    // pairs, 10.4 split, 2000 x 8192 x 512 (64, 32) 13.0 and 14.8.  Unsplit it loads twice the
+    // operands that the pairs do for a product: 1664 x 65536 x 1408 (143 tiles, 256 slices)
+    // 86 us split in two, 92 with pairs, 1664 x 65536 x 1536 (156, 256) 118 unsplit, 89 with pairs.
+    int dev;
+    W8A8_TRY(current_device(dev));
     const int64_t tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-    if (tiles <= p.slices)
+    if (tiles <= p.slices && tiles <= g_dev[dev].sms)
         return launch_fp4_skinny<kFmt, 128, false>(x, nullptr, w, p, stream);
     return p.N % 8 == 0 && aligned16(p.y) ? launch_fp4_pair<kFmt, true>(x, w, p, stream)
                                           : launch_fp4_pair<kFmt, false>(x, w, p, stream);

@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                 bool ok = true;
                 for (int t = pair; ok && t < num_units; t += pairs, ++i) {
                     const bool whole = t < p.num_full;
-                    // tile i - 2 has left this accumulator, tile i - 1 the columns both use
+                    // tile i - 2 has left this accumulator, tile i - 1 the columns both use (with
+                    // kTma the second implies the first: all warps arrive there, tile by tile)
                     if (i > 1 && !gemm::gemm_wait(&sm.tdrained[i & 1], ((i >> 1) - 1) & 1, abort))
                         break;
                     if (i > 0 && !gemm::gemm_wait(&sm.tshared, (i - 1) & 1, abort))

@@ -11,18 +11,19 @@
 // in FP32, rounded at h' and n alone; the second norm reads h' as it is stored.  The 4-bit
 // output is that of the quantizer of fp4.cuh on n, code for code.
 //
-// Bound by HBM: h and y are read, h' and n written once (8 bytes a value, 6.6 with 4-bit
-// output).  W warps share a row and keep its h and y, then h' and n, in registers, P pieces
+// With BF16 output bound by HBM: h and y are read, h' and n written once (8 bytes a value, 6.6
+// with 4-bit output).  W warps share a row and keep its h and y, then h' and n, in registers, P pieces
 // of 8 values a lane; the sums of squares go through shuffles and shared memory.  32768 x 4096
-// with all factors: 168 us (6.4 TB/s), 192 with NVFP4 and 176 with MXFP4 output (4.6 and 5.0:
-// the reductions' barriers and the conversions); 1 x 4096 2.2 us.
+// with all factors: 168 us (6.4 TB/s), 193 with NVFP4 and 175 with MXFP4 output (4.6 and 5.0;
+// neither HBM nor issue is full there: the latency of a row's reductions, three in turn, at 16
+// warps a SM); 1 x 4096 2.3 us.
 //
 //   stream_kernel  many rows: CTAs stay, take every gridDim.x-th row, and have the next rows'
 //                  h and y copied into a ring in shared memory (one bulk copy each) while they
 //                  work.  A lane has the same columns in every row: for P <= 2 their factors
 //                  stay in registers and are read again when the rows' group b changes; for
 //                  more they come from L1 or L2 for each row, ahead of the wait for the row and
-//                  of the second sum (4096 x 16384 nvfp4: 165 us; where they are used, 219).
+//                  of the second sum (4096 x 16384 nvfp4: 160 us; where they are used, 219).
 //   row_kernel     few rows, or rows too long for the ring: one row a W warps, straight from
 //                  global memory; longer rows are read again for each pass (kLong).
 #pragma once

@@ -25,8 +25,9 @@
 //        different whole numbers, the larger below 32 * 2^8 or 7 * 2^12, differ by one.  The
 //        products with reciprocals below are within 2^-21 of the quotients (three roundings
 //        and two reciprocals good to one unit in the last place).  Rounded to 17 significant
-//        bits (scale), or to a multiple of 2^-17 (code: at most 8, boundaries from 0.25 up),
-//        they lie on a boundary only if the quotient does, and on the same side otherwise.
+//        bits (scale), or to a multiple of 2^-17 (code: below 9.1, the most where a scale is
+//        rounded down to E4M3's smallest; boundaries from 0.25 to 5), they lie on a boundary
+//        only if the quotient does, and on the same side otherwise.
 //        (A negative value below 2^-18 of the unit becomes +0 on the way, others -0.)
 //
 // Scales lie as tcgen05 block-scaled products read them: 512-byte tiles of 128 rows x 4

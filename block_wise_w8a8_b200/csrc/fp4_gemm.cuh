@@ -148,8 +148,8 @@ __device__ __forceinline__ bool elect_one()
 // Tile 256 x 256, two CTAs of a cluster together (cta_group::2): each holds 128 rows of x and
 // 128 rows of w in shared memory and the accumulator of its 128 rows of y x all 256
 // columns in its tensor memory; the even CTA's MMA thread issues the products for both.
-// A slice then costs each SM 32 KB of codes and 4-6 KB of scales for 128 x 256 x 256
-// products.  One thread of each CTA loads its own half (signalling the even CTA's
+// A slice then costs each SM 32 KB of codes and 3 KB (kMx) or 6 KB (kNv) of scales for 128 x
+// 256 x 256 products.  One thread of each CTA loads its own half (signalling the even CTA's
 // barrier), the epilogue warps of each store their 128 rows.
 //
 // kTma: four epilogue warps, 64 columns at a time through shared memory to TMA stores.
@@ -170,10 +170,13 @@ __device__ __forceinline__ bool elect_one()
 // round: 256 x 4096 x 4096, 16 tiles on 74 pairs, 11.1 -> 8.9 us; 4096^3 (mxfp4), 3.5 rounds
 // in place of 4, 33.9 -> 32.2 us.  With kTma only.
 //
-// 16384 x 4096 x 16384: 409 us in a burst (81% of four times the BF16 rate), 465 back to back
-// under the power cap (sw_power_cap; SM clock about 1.5 GHz); 8192^3 185 us (90%), mxfp4 175
-// (95%).  Bound by the products: a tile takes 9350 cycles, 8192 of them its products at the
-// full rate.
+// 16384 x 4096 x 16384: 393 to 411 us in a burst (81 to 84% of four times the BF16 rate), 456 to
+// 511 back to back; 8192^3 184 us (90%), mxfp4 175 (95%).  Bound by the products and by the power
+// limit that sets their clock, in a single call too (%clock64 against %globaltimer in a copy of
+// the kernel: 1.32 GHz in the burst, 1.08 back to back; mxfp4 1.38 and 1.14).  A tile of 16
+// slices takes 9340 cycles: 525 a slice (mxfp4 513; 512 at the full rate) and 940 in which the
+// next tile waits for the shared columns.  4096^3 takes 41,000 cycles at 1.5 GHz: 3700 up to
+// the first slice, 34,400 for 3.5 tiles, 2600 for the last epilogue.
 constexpr int kPairStages = 5;
 constexpr int kPairGroup = 8;                // M tiles of a raster group
 

@@ -372,11 +372,11 @@ W8A8_API size_t w8a8_fp4_linear_workspace_bytes(int64_t M, int64_t K, int format
 /* Y[M, N] = X[M, K] W^T + bias with X quantized in the call to the weight's format:
  *     y[m,n] = bf16( factor_x[m] factor_w[n] * sum_k value_x[m,k] value_w[n,k] + bias[n] ),
  *   values without factors, FP32 accumulation, one rounding to BF16; the sum's order is fixed
- *   by M, N and K.  Factors whose product leaves FP32's normal range are applied one after the
- *   other, so that only the result's own range counts.  Guard: the 4-bit path runs iff K is a multiple of 32 up to 2^24, the weight
- *   has codes and x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and
- *   without that copy the call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M
- *   and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,
+ *   by M, N and K on a device.  Factors whose product leaves FP32's normal range are applied
+ *   one after the other, so that only the result's own range counts.
+ *   Guard: the 4-bit path runs iff K is a multiple of 32 up to 2^24, the weight has codes and
+ *   x is 16-byte aligned; otherwise the BF16 GEMM runs on w->w_bf16, and without that copy the
+ *   call fails with W8A8_ERR_SHAPE (W8A8_ERR_ALIGNMENT for x).  Any M and N.  workspace: 16-byte aligned, w8a8_fp4_linear_workspace_bytes(M, K, format) bytes,
  *   else W8A8_ERR_WORKSPACE; may be NULL on the BF16 path.  Calls that may be in flight at
  *   once (two streams, two captured graphs) need workspaces of their own.  path_taken as for
  *   w8a8_linear. */

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
         }
         if (r + gridDim.x >= p.M)
             fp4::let_next_start();
-        mbar_wait(&sm.full[s], phase, abort);        // how a ring ends: fp4::hold_ring
+        mbar_wait(&sm.full[s], phase, abort);        // that gives up: see fp4::quantize_stream_kernel
         const uint8_t *slot = ring + static_cast<size_t>(s) * 2 * row_bytes;
         uint32_t y[P][4], h[P][4];
 #pragma unroll
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(W * 32, P > 2 ? 1 : kStreamWarps / W) stream_k
     if constexpr (kOut != kOutBf16)
         fp4::zero_scales(p.scales, p.M, p.M_pad, KT, blockIdx.x, gridDim.x);
     if (threadIdx.x == 0 && *abort)
-        fp4::hold_ring();
+        fp4::hold_smem();
 }
 
 // ------------------------------------------------------------------ few or long rows

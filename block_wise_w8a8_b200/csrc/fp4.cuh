@@ -283,6 +283,16 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *s, int warp, u
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
+// By one thread of a CTA whose wait gave up, at the CTA's end: copies in flight land before its
+// shared memory is released, for it may be another CTA's next.  They need microseconds, this
+// waits a millisecond.
+__device__ __forceinline__ void hold_smem()
+{
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull)
+        ;
+}
+
 struct QParams {
     const uint16_t *x;       // [rows, K] BF16
     int64_t rows, rows_pad;  // rows_pad: rows rounded up to 128 (the scale tiles' rows)
@@ -398,15 +408,7 @@ struct StreamTail {                              // behind the ring
 // and behind it thread 0, finding it up, fills no slot again, for the copy into this one may
 // still be in flight and its barrier's phase open.  The rows from there on are worked on as
 // they are, so that every warp reaches every barrier; their waits give up at once.  Last,
-// thread 0 holds the CTA's shared memory, which may be another CTA's next, until the copies in
-// flight have landed: they need microseconds, it waits a millisecond.
-__device__ __forceinline__ void hold_ring()
-{
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull)
-        ;
-}
-
+// thread 0 holds the shared memory (hold_smem).
 template <int kFmt, int W>
 __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kernel(const QParams p)
 {
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(W * 32, kStreamWarps / W) quantize_stream_kern
     }
     zero_scales(p.scales, p.rows, p.rows_pad, KT, blockIdx.x, gridDim.x);
     if (threadIdx.x == 0 && *abort)
-        hold_ring();
+        hold_smem();
 }
 
 // y [rows, K] BF16 = the values the codes stand for: fl(code * scale) is exact, the product

@@ -384,13 +384,6 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!ok) {
-                // copies in flight land before shared memory is released: they need
-                // microseconds, the end of the kernel waits a millisecond for them
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 1000000ull)
-                    ;
-            }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
@@ -618,6 +611,10 @@ __global__ void __launch_bounds__(PairEpi<kTma>::kThreads, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
+    // a wait of any thread gave up (the producer may have issued its last loads before that):
+    // copies in flight land before shared memory is released
+    if (threadIdx.x == 0 && *abort)
+        hold_smem();
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -804,13 +801,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 
     if (warp == 0) {
         uint32_t it = 0;
-        bool ok = true;
         for (int ks = ks0; ks < ks1; ++ks, ++it) {
             const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-            if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort)) {
-                ok = false;
+            if (!gemm::gemm_wait(&sm.empty[s], ph ^ 1, abort))
                 break;
-            }
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.full[s], kTxBytes);
                 tma_load_2d(sm.w[s], &tmW, &sm.full[s], ks * 128, tn * 128);
@@ -827,13 +821,6 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         // N = 4096 5.7, 4.7, 4.8).  The pair kernel gains as much before another product, but
         // loses it before a quantizer (linear of 128 x 4096 x 16384: 16.5 -> 17.0 us).
         let_next_start();
-        if (!ok) {
-            // copies in flight land before shared memory is released: they need
-            // microseconds, this waits a millisecond for them
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < 1000000ull)
-                ;
-        }
     } else if (warp == 1) {
         if (elect_one()) {
             const uint32_t w0 = operand_lo(sm.w[0]), x0 = operand_lo(sm.x[0]);
@@ -978,6 +965,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     }
     if (warp == 1)
         tmem_dealloc(tmem, kCols);
+    // as at the end of the pair kernel
+    if (threadIdx.x == 0 && *abort)
+        hold_smem();
 }
 
 } // namespace fp4

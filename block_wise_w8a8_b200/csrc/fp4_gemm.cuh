@@ -642,6 +642,7 @@ struct alignas(1024) SkinnySmem {
     uint64_t full[kStages];
     uint64_t empty[kStages];
     uint64_t tfull;
+    uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
     uint32_t top[4][4];                  // kQuant: per warp and row, the largest magnitude
@@ -769,6 +770,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
             mbar_init(&sm.empty[s], 1);
         }
         mbar_init(&sm.tfull, 1);
+        mbar_init(&sm.mma_done, 1);
         sm.abort = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmW);
@@ -854,6 +856,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
                     ph ^= 1;
                 }
             }
+            // every product issued here completes before tensor memory is released, also where
+            // this thread or the epilogue gave up
+            umma_commit(&sm.mma_done);
+            volatile int no_abort = 0;
+            mbar_wait(&sm.mma_done, 0, &no_abort, 100000000ull);
         }
         __syncwarp();
     } else if (kQuant) {

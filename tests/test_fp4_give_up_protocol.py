@@ -6,7 +6,11 @@ be another CTA's by then.
 The producer may have issued its last loads, and be done, when the issuing thread gives up on
 one of them.  So not the producer's own waits say whether the CTA has to stay: at the block
 barrier that everybody reaches the flag of any wait that gave up is final, and behind it one
-thread, finding it up, stays until the loads in flight have landed."""
+thread, finding it up, stays until the loads in flight have landed.
+
+Nor may tensor memory be released, behind that barrier, with products in flight, as they may be
+when the issuing thread or the epilogue gives up, on a load or because another warp has: the
+issuing thread waits for its own in any case."""
 import random
 
 import pytest
@@ -18,7 +22,8 @@ class Broken(AssertionError):
 
 def run(slices, stages, seed, late=0.0, form="mended"):
     """One schedule; True if a wait gave up.  Forms: "mended"; "producer": the producer stays if a
-    wait of its own gave up, and nobody else; "early": the flag is read before the barrier."""
+    wait of its own gave up, and nobody else; "early": the flag is read before the barrier;
+    "issuer": the issuing thread does not wait for its products."""
     rng = random.Random(seed)
     full, empty = [0] * stages, [0] * stages           # completed phases
     tfull = [0]
@@ -45,8 +50,14 @@ def run(slices, stages, seed, late=0.0, form="mended"):
         here[0] += 1
         while here[0] < 3:
             yield
-        if form == "mended" and who == "producer" and raised[0]:
+        if form in ("mended", "issuer") and who == "producer" and raised[0]:
             yield from hold()
+
+    def other():
+        """Another warp's wait gives up, at any time."""
+        for _ in range(rng.randrange(10, 400)):
+            yield
+        raised[0] = True
 
     def producer():
         ok = True
@@ -70,14 +81,19 @@ def run(slices, stages, seed, late=0.0, form="mended"):
             if it == slices - 1:
                 queue.append(("tfull", 0))
             yield
+        while queue and form != "issuer":
+            yield
         yield from barrier("issuer")
+        if queue:
+            raise Broken("tensor memory released with products in flight")
 
     def epilogue():
         yield from wait(lambda: tfull[0] > 0)
         yield from barrier("epilogue")
 
-    agents = [producer(), issuer(), epilogue()]
+    agents = [producer(), issuer(), epilogue()] + ([other()] if late and rng.random() < 0.5 else [])
     weights = [rng.choice((1, 1, 4)) for _ in agents]
+    pipe = rng.choice((0.3, 0.3, 0.01))
     for _ in range(60000):
         if not agents:
             if landing:
@@ -88,7 +104,7 @@ def run(slices, stages, seed, late=0.0, form="mended"):
         for c in [c for c in landing if c[1] <= 0]:
             landing.remove(c)
             full[c[0]] += 1
-        if queue and rng.random() < 0.3:
+        if queue and rng.random() < pipe:
             kind, s = queue.pop(0)
             if kind == "empty":
                 empty[s] += 1
@@ -111,8 +127,8 @@ def test_every_schedule_ends(slices, stages):
     assert stops > 5, "the schedules reach the case"
 
 
-@pytest.mark.parametrize("form", ["producer", "early"])
-def test_another_place_for_the_stay_is_caught(form):
+@pytest.mark.parametrize("form", ["producer", "early", "issuer"])
+def test_another_form_is_caught(form):
     caught = 0
     for seed in range(100):
         try:

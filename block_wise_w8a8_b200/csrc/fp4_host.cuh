@@ -253,7 +253,7 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
     auto kern = fp4::gemm_skinny_kernel<kFmt, BT, kQuant>;
     constexpr size_t smem = fp4::kSkinnySmemBytes<kFmt, BT>;
     static_assert(smem <= 232448, "exceeds the 227 KB of shared memory a CTA may use");
-    int clusters[3];
+    int clusters[2];
     constexpr int slot = kFmt * 5 + (kQuant ? 4 : BT == 16 ? 0 : BT == 32 ? 1 : BT == 64 ? 2 : 3);
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -264,7 +264,7 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
                 return cuda_fail(e);
             g_dev[dev].fp4_skinny_attr_set[slot] = true;
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             int &n = g_dev[dev].fp4_clusters[i];
             const int size = 2 << i;
             if (n == 0) {
@@ -287,15 +287,18 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
             clusters[i] = n;
         }
     }
-    // K is split while the clusters fit on the device all at once, two CTAs a SM (the occupancy
-    // query counts one), and leave each CTA enough slices: 4 in clusters of up to 4 (1 x 4096 x
-    // 4096: 7.7 us unsplit, 6.7, 6.0 in clusters of 2, 4 and 7.4 of 8), 8 in clusters of 8
-    // (1 x 16384 x 3584, 28 tiles: 9.1 us in clusters of 4, 8.4 of 8).  A cluster takes SMs of
-    // one group (GPC), whose number its size need not divide: of 148 SMs clusters of 4 use 132
-    // and of 8 120, and tiles past that run in a second wave (37 x 16384 x 4608, 36 tiles: 13.7 us
-    // in clusters of 4, 20.4 of 8; 37 x 4096 x 9216, 72 tiles: 8.1 us of 2, 14.1 of 4).
+    // K is split while the clusters fit on the device all at once, two CTAs a SM, and leave each
+    // CTA enough slices: 4 in clusters of up to 4 (1 x 4096 x 4096: 7.7 us unsplit, 6.7, 6.0 in
+    // clusters of 2, 4 and 7.4 of 8), 8 in clusters of 8 (1 x 16384 x 3584, 28 tiles: 9.1 us in
+    // clusters of 4, 8.4 of 8).  A cluster takes SMs of one group (GPC), whose number its size need
+    // not divide, and tiles past those that fit run in a second wave (37 x 16384 x 4608, 36 tiles:
+    // 13.7 us in clusters of 4, 20.4 of 8; 37 x 4096 x 9216, 72 tiles: 8.1 us of 2, 14.1 of 4).
+    // The occupancy query counts one CTA a SM, 74 clusters of 2 and 33 of 4.  With two CTAs a SM
+    // clusters of 8 and 4 take the SMs that those take there: 33 and, three fewer, 71 were seen
+    // to run at once (34 and 72 not).
     int splits = 1;
-    for (int i = 0; i < 3 && tiles <= 2 * clusters[i] && p.slices >= splits * 2 * (splits < 4 ? 4 : 8); ++i)
+    const int fit[3] = {2 * clusters[0], clusters[0] - 3, clusters[1]};
+    for (int i = 0; i < 3 && tiles <= fit[i] && p.slices >= splits * 2 * (splits < 4 ? 4 : 8); ++i)
         splits *= 2;
     return launch_dependent(kern, tiles * splits, fp4::kSkinnyThreads, smem, stream, splits, mx, mw, mxs, mws, xb, p);
 }

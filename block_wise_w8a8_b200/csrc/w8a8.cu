@@ -39,7 +39,7 @@ struct DeviceInfo {
     bool norm_stream_attr_set[3][19] = {};                 // bnorm::stream_kernel by output and warps (17, 18: 3, 4 pieces)
     bool fp4_stream_attr_set[2][17] = {};                  // fp4::quantize_stream_kernel by format and warps
     bool fp4_skinny_attr_set[10] = {};                     // by format and token tile, quantizing or not
-    int fp4_clusters[3] = {};                              // clusters of 2, 4, 8 that fit with a CTA a SM
+    int fp4_clusters[2] = {};                              // clusters of 2, 4 that fit with a CTA a SM
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;

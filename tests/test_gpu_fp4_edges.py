@@ -54,7 +54,7 @@ def _check(y, x, w, bias):
 SHAPES = [(3, 512, 264), (3, 4096, 100), (40, 512, 264), (300, 512, 264), (300, 512, 263), (700, 96, 1000)]
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 16384, 30 * 128), (1, 16384, 31 * 128), (37, 16384, 36 * 128), (1, 4096, 66 * 128), (1, 4096, 67 * 128),
+@pytest.mark.parametrize("M,K,N", [(1, 16384, 33 * 128), (1, 16384, 34 * 128), (37, 16384, 36 * 128), (1, 4096, 71 * 128), (1, 4096, 72 * 128),
                                    (20, 4096, 72 * 128), (3, 2048, 148 * 128), (3, 2048, 149 * 128), (768, 16384, 768), (1664, 37120, 1408),
                                    (1664, 40960, 1536)])
 def test_sizes_around_the_limits_of_splitting(M, K, N):

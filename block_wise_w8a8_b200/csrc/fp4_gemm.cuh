@@ -113,7 +113,7 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo)
 // of 2^-30), and a zero sum would meet an infinity.  v then takes one factor after the other.
 // Both are above 1 or both below 2^-14 at such a place, and |v| is 0 or at least 2^-20: v wf
 // overflows, or loses bits, only where the result does.  A warp tests the range of its factors
-// once (products of few tokens +1% in time, many 0 to 2%; tested at each output 10 to 40%); an
+// once (up to 2% of the time of many tokens, none of few; tested at each output 10 to 40%); an
 // output depends on its own v and factors alone.
 __device__ __forceinline__ bool normal_range(float p)
 {
@@ -800,6 +800,25 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     const uint32_t tmem = sm.tmem_base;
     if (!kQuant)
         asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The epilogue's thread owns output n and the tokens of this CTA's tile.  Its column's factor
+    // and bias are fetched ahead where the factor is looked at before the accumulator is complete.
+    float *part = reinterpret_cast<float *>(sm.w);
+    const int row = (warp & 3) * 32 + static_cast<int>(lane);
+    const int64_t n = static_cast<int64_t>(tn) * 128 + row;
+    const int64_t m0 = static_cast<int64_t>(tm) * BT;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(BT), p.M - m0));
+    const bool store = warp >= 2 && n < p.N;
+    float wf = 1.0f, bias = 0.0f;
+    auto fetch_column = [&]() {
+        if (store) {
+            if (kFmt == kNv)
+                wf = __ldg(p.wf + n);
+            if (p.bias != nullptr)
+                bias = __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16);
+        }
+    };
+    if (!kQuant)
+        fetch_column();
 
     if (warp == 0) {
         uint32_t it = 0;
@@ -866,42 +885,32 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     } else if (kQuant) {
         quantize_slices<kFmt>(sm, p, x, ks0, ks1, warp - 2, lane, abort);
     }
-    // The epilogue's thread owns output n and the tokens of this CTA's tile.
-    float *part = reinterpret_cast<float *>(sm.w);
-    const int row = (warp & 3) * 32 + static_cast<int>(lane);
-    const int64_t n = static_cast<int64_t>(tn) * 128 + row;
-    const int64_t m0 = static_cast<int64_t>(tm) * BT;
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(BT), p.M - m0));
-    const bool store = warp >= 2 && n < p.N;
-    float wf = 1.0f, bias = 0.0f;
-    if (store) {
-        if (kFmt == kNv)
-            wf = __ldg(p.wf + n);
-        if (p.bias != nullptr)
-            bias = __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16);
-    }
-    // the products of the warp's rows' factors with all of the tokens'
-    uint32_t xf_min = 0x3F800000u, xf_max = xf_min;
-    if (kFmt == kNv && warp >= 2)
+    if (kQuant)
+        fetch_column();
+    // Whether the products of the warp's columns' factors with the tokens' are all in range.  kQuant
+    // has few outputs a thread and tests at each: the factors come late there, and reductions
+    // over them would be waited for (4 x 4096 x 4096: 6.3 us for 6.5).
+    bool plain = true;
+    if (kFmt == kNv && !kQuant && warp >= 2) {
+        uint32_t xf_min = 0x3F800000u, xf_max = xf_min;
         for (int t = static_cast<int>(lane); t < tokens; t += 32) {
-            const uint32_t f = __float_as_uint(kQuant ? sm.factor[t] : __ldg(p.xf + m0 + t));
+            const uint32_t f = __float_as_uint(__ldg(p.xf + m0 + t));
             xf_min = min(xf_min, f);
             xf_max = max(xf_max, f);
         }
-    const bool all_plain =
-        kFmt != kNv || warp < 2 || normal_products(xf_min, xf_max, __float_as_uint(wf), __float_as_uint(wf));
-    auto finish = [&](auto plain, float v, int t) {
-        const int64_t m = m0 + t;
-        const float xf = kFmt == kNv ? (kQuant ? sm.factor[t] : __ldg(p.xf + m)) : 1.0f;
+        plain = normal_products(xf_min, xf_max, __float_as_uint(wf), __float_as_uint(wf));
+    }
+    auto finish = [&](float v, int t) {
         if (kFmt != kNv)
             v = v + bias;
-        else if (decltype(plain)::value)
-            v = fmaf(v, xf * wf, bias);
+        else if (kQuant)
+            v = scaled(v, sm.factor[t], wf, bias);
         else
-            v = scaled(v, xf, wf, bias);
-        p.y[m * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+            v = fmaf(v, __ldg(p.xf + m0 + t) * wf, bias);
+        p.y[(m0 + t) * p.N + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
     };
-    auto from_tmem = [&](auto plain) {
+    if (warp >= 2 && gemm::gemm_wait(&sm.tfull, 0, abort)) {
+        tc_fence_after();
         const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
         for (int c = 0; c < tokens; c += 16) {
@@ -910,28 +919,22 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
             tmem_wait_ld(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                if (splits > 1)
+                if (splits > 1 || !plain)
                     part[(c + i) * 128 + row] = __uint_as_float(v[i]);
                 else if (store && c + i < tokens)
-                    finish(plain, __uint_as_float(v[i]), c + i);
+                    finish(__uint_as_float(v[i]), c + i);
             }
         }
-    };
-    if (warp >= 2 && gemm::gemm_wait(&sm.tfull, 0, abort)) {
-        tc_fence_after();
-        if (splits > 1 || all_plain)
-            from_tmem(std::true_type{});
-        else if constexpr (kFmt == kNv)
-            from_tmem(std::false_type{});
     }
     tc_fence_before();
     __syncthreads();
-    if (splits > 1) {
+    if (splits > 1)
         norm::cluster_barrier();     // every rank's partial tile is in its shared memory
+    if (splits > 1 || !plain) {
         // tokens are dealt out to the ranks in equal runs
         const int each = (tokens + splits - 1) / splits;
         const int t1 = min(tokens, (rank + 1) * each);
-        auto join = [&](auto plain) {
+        if (store && plain && !*abort) {
             // 8 tokens of 4 ranks in flight: a read of another SM's shared memory takes about
             // as long as one of L2
             for (int t0 = rank * each; t0 < t1; t0 += 8) {
@@ -959,17 +962,28 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (t0 + i < t1)
-                        finish(plain, v[i], t0 + i);
+                        finish(v[i], t0 + i);
             }
-        };
-        if (store && !*abort) {
-            if (all_plain)
-                join(std::true_type{});
-            else if constexpr (kFmt == kNv)
-                join(std::false_type{});
+        } else if (kFmt == kNv && !kQuant && store && !*abort) {
+            // the same sums, one after the other, where a product of factors is out of range
+#pragma unroll 1
+            for (int t = rank * each; t < t1; ++t) {
+                float v = 0.0f;
+#pragma unroll 1
+                for (int q = 0; q < splits; ++q) {
+                    float u;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u)
+                                 : "r"(map_to(smem_u32(part + t * 128 + row), static_cast<uint32_t>(q))));
+                    v += u;
+                }
+                p.y[(m0 + t) * p.N + n] =
+                    static_cast<uint16_t>(pack_bf16x2(scaled(v, __ldg(p.xf + m0 + t), wf, bias), 0.0f) & 0xFFFFu);
+            }
         }
-        norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
     }
+    if (splits > 1)
+        norm::cluster_barrier();     // no CTA leaves while another reads its partial tile
     if (warp == 1)
         tmem_dealloc(tmem, kCols);
     // as at the end of the pair kernel

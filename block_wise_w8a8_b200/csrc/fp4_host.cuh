@@ -288,7 +288,6 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
         }
     }
     // K is split while the clusters fit on the device all at once, two CTAs a SM, and leave each
-<<<<<<< Updated upstream
     // CTA enough slices: 4 in clusters of up to 4 (1 x 4096 x 4096: 7.7 us unsplit, 6.7, 6.0 in
     // clusters of 2, 4 and 7.4 of 8), 8 in clusters of 8 (1 x 16384 x 3584, 28 tiles: 9.1 us in
     // clusters of 4, 8.4 of 8).  A cluster takes SMs of one group (GPC), whose number its size need
@@ -299,19 +298,6 @@ w8a8_status_t launch_fp4_skinny(const Fp4Operand &x, const uint16_t *xb, const F
     // to run at once (34 and 72 not).
     int splits = 1;
     const int fit[3] = {2 * clusters[0], clusters[0] - 3, clusters[1]};
-=======
-    // CTA enough slices: 4 in clusters of up to 4 (1 x 4096 x
-    // 4096: 7.7 us unsplit, 6.7, 6.0 in clusters of 2, 4 and 7.4 of 8), 8 in clusters of 8
-    // (1 x 16384 x 3584, 28 tiles: 9.1 us in clusters of 4, 8.4 of 8).  A cluster takes SMs of
-    // one group (GPC), whose number its size need not divide, and tiles past those that fit run
-    // in a second wave (37 x 16384 x 4608, 36 tiles: 13.7 us in clusters of 4, 20.4 of 8; 37 x 4096
-    // x 9216, 72 tiles: 8.1 us of 2, 14.1 of 4).  The occupancy query counts one CTA a SM: 74
-    // clusters of 2, 33 of 4.  With two a SM a cluster of 8 takes as many SMs as one of 4 there,
-    // and 33 fit in fact; of clusters of 4 and 2 at least twice as many fit (71 of 4 in fact, but
-    // from 67 tiles on clusters of 2 are faster).
-    int splits = 1;
-    const int fit[3] = {2 * clusters[0], 2 * clusters[1], clusters[1]};
->>>>>>> Stashed changes
     for (int i = 0; i < 3 && tiles <= fit[i] && p.slices >= splits * 2 * (splits < 4 ? 4 : 8); ++i)
         splits *= 2;
     return launch_dependent(kern, tiles * splits, fp4::kSkinnyThreads, smem, stream, splits, mx, mw, mxs, mws, xb, p);
